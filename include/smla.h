@@ -323,6 +323,158 @@ int smla_flash_mla_with_kvcache_static_scratch(const void* q, const uint8_t* kvc
                                                int num_sm_parts, float softmax_scale, int batch, int s_q, int h_q,
                                                int topk, void* o, float* lse, uint32_t* status_out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged serving of grouped-query attention: block tables and slot maps built
+ * on the GPU, a block-scaled 8-bit KV cache with its writer, and attention
+ * over it.  Block size 64 as for the MLA caches, so one table and one free
+ * list serve both.
+ * ------------------------------------------------------------------------- */
+
+/* Code types of a block-scaled cache. */
+#define SMLA_Q8_E4M3 0
+#define SMLA_Q8_INT8 1
+
+/*
+ * A KV cache in blocks of 64 tokens: codes [num_blocks][h_kv][64][head_dim]
+ * (8 bits each) and one float32 scale for each (block, head); a key or value
+ * is code * scale.  Blocks may be strided (one allocation for keys and
+ * values, for instance); within a block the codes are dense.
+ *   k_cache, v_cache : device, 16-byte aligned
+ *   k_scale, v_scale : device float32 [num_blocks][h_kv]; finite, >= 0, those
+ *                      of one request and head within 2^60 of one another
+ *   *_block_stride   : bytes between blocks, a multiple of 16
+ *   *_scale_stride   : floats between the scales of neighbouring blocks
+ *   head_dim         : 64 or 128;  h_kv * head_dim * 64 < 2^31
+ *   format           : SMLA_Q8_E4M3 or SMLA_Q8_INT8
+ */
+typedef struct {
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_blocks;
+  int64_t k_block_stride, v_block_stride;
+  int64_t k_scale_stride, v_scale_stride;
+  int h_kv, head_dim, format;
+} smla_q8_cache;
+
+/*
+ * Give the requests of a step the blocks of their new tokens and map every new
+ * token to its cache row.  Request r holds cache_seqlens[r] tokens in the
+ * first ceil(cache_seqlens[r] / 64) entries of its table row and takes
+ * new_lens[r] more (negative counts as 0); fresh blocks come off the end of
+ * the free list, request by request:
+ *   entry ceil(len / 64) + i = free_blocks[num_free - 1 - (blocks of the
+ *                              requests before r) - i].
+ * A request fits if its blocks are covered by num_free, its row has room for
+ * them and its tokens end within max_new_tokens; one that does not keeps its
+ * length and its table row, and its tokens get slots -1.
+ *   block_table   : device int32 [batch][max_blocks], fresh entries written
+ *   cache_seqlens : device int32 [batch], before the new tokens
+ *   new_lens      : device int32 [batch]
+ *   free_blocks   : device int32 [free_capacity], read
+ *   num_free      : device int32 [1], entries of free_blocks in use
+ *   slot_mapping  : device int64 [max_new_tokens], written: block * 64 + offset
+ *                   of each new token in (request, position) order, -1 for the
+ *                   tokens of a request that did not fit and behind the last
+ *   cu_new        : device int32 [batch + 1], written: new tokens before each
+ *                   request
+ *   seqlens_out   : device int32 [batch], written: the lengths with the tokens
+ *   num_free_out  : device int32 [1], written: entries left on the free list
+ * The inputs are only read (besides fresh table entries), so a call may be
+ * repeated; outputs must not overlap inputs.  slot_mapping is the one that
+ * smla_quantize_kv takes; cu_new and seqlens_out are what
+ * smla_quantize_kv_blocks and smla_gqa_attention_with_kvcache take.
+ */
+int smla_extend_block_table(int32_t* block_table, int max_blocks, const int32_t* cache_seqlens,
+                            const int32_t* new_lens, int batch, const int32_t* free_blocks, int64_t free_capacity,
+                            const int32_t* num_free, int64_t max_new_tokens, int64_t* slot_mapping, int32_t* cu_new,
+                            int32_t* seqlens_out, int32_t* num_free_out, void* stream);
+
+/*
+ * Write new tokens into a block-scaled cache.  Tokens cu_new[r] ..
+ * cu_new[r + 1] - 1 of k and v go to positions cache_seqlens[r] .. of request
+ * r.  A request whose new_seqlens[r] - cache_seqlens[r] differs from its token
+ * count (one that got no blocks) is left alone.  For each (block, head)
+ * written, with `was` its scale if the block holds older tokens, else 0:
+ *   s    = smallest power of two (>= 2^-126) at which the largest finite
+ *          magnitude among the new values is <= 448 (e4m3) or 127 (int8); 0 if
+ *          all are zero
+ *   now  = max(s, was), stored
+ *   code = x / now rounded to nearest even and saturated (all 0 for now = 0);
+ *          NaN is stored as NaN (e4m3) or 0 (int8), infinities saturate
+ * and where now > was the older codes become round(code * (was / now)).
+ * Rows behind the last token are left as they were.  No two requests of a call
+ * may write to the same block.
+ *   k, v          : device bf16 [total_new][h_kv][head_dim] with the given
+ *                   token and head strides (elements, multiples of 8); 16-byte
+ *                   aligned
+ *   cache         : host struct; codes and scales written
+ *   block_table   : device int32 [batch][max_blocks]
+ *   cache_seqlens, new_seqlens : device int32 [batch], before and with the tokens
+ *   cu_new        : device int32 [batch + 1]
+ *   status        : device uint32, sticky flags as in a workspace's status word
+ *                   (see smla_get_device_status), or NULL: a block outside the
+ *                   table or the cache is skipped and flagged, token offsets
+ *                   that are not increasing within total_new likewise
+ */
+int smla_quantize_kv_blocks(const void* k, const void* v, int64_t k_token_stride, int64_t k_head_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, int64_t total_new,
+                            const smla_q8_cache* cache, const int32_t* block_table, int max_blocks, int batch,
+                            const int32_t* cache_seqlens, const int32_t* new_seqlens, const int32_t* cu_new,
+                            uint32_t* status, void* stream);
+
+/* Workspace bytes of smla_gqa_attention_with_kvcache (split partials; no state
+ * is kept in it between calls) for head_dim on `device`; 0 for bad arguments. */
+size_t smla_gqa_workspace_bytes(int head_dim, int device);
+
+/*
+ * Grouped-query attention of the new tokens of each request over a
+ * block-scaled cache that already holds them.  Request r has the query tokens
+ * cu_seqlens_q[r] .. cu_seqlens_q[r + 1] - 1 (or s_q each, where cu_seqlens_q
+ * is NULL), the last n of its cache_seqlens[r] positions: token t stands at
+ * p = cache_seqlens[r] - n + t.  For query head h (KV head h / (h_q / h_kv))
+ * over the positions j that the token sees:
+ *   x_j = softmax_scale * <q, k_j>
+ *   x_j = softcap * tanh(x_j / softcap)            with softcap > 0
+ *   x_j = x_j - alibi_slopes[h] * |p - j|          with alibi_slopes
+ *   lse = ln(sum_j exp(x_j)),  o = sum_j exp(x_j - lse) v_j
+ * (-inf and 0 where the token sees nothing).  It sees 0 <= j <
+ * cache_seqlens[r] with
+ *   causal      : j <= p, or j < prefix_lens[r]   (the prefix sees itself in
+ *                 both directions)
+ *   doc_bounds  : doc_bounds[token][0] <= j < doc_bounds[token][1]
+ * q, the probabilities (f16, after an fp32 softmax) and the codes enter the
+ * tensor cores, accumulated in fp32.  Output is bitwise reproducible.
+ *   q            : device bf16 [total_q][h_q][head_dim] with the given strides
+ *                  (elements, multiples of 8), 16-byte aligned
+ *   cache        : host struct; read
+ *   max_seqlen_q : host hint, the most query tokens of a request; it picks the
+ *                  kernel and does not change what is computed
+ *   softmax_scale: <= 0 or NaN selects 1/sqrt(head_dim);  softcap: 0 = none
+ *   alibi_slopes : device float32 [h_q] or NULL
+ *   prefix_lens  : device int32 [batch] or NULL (needs causal)
+ *   doc_bounds   : device int32 [total_q][2] or NULL, 8-byte aligned
+ *   o            : device bf16 [total_q][h_q][head_dim], dense, 16-byte aligned
+ *   lse          : device float32 [total_q][h_q], natural log
+ *   workspace    : device, >= smla_gqa_workspace_bytes, 256-byte aligned; calls
+ *                  that may run at the same time need workspaces of their own
+ *   status       : as for smla_quantize_kv_blocks
+ * h_q is a multiple of h_kv; total_q * h_q < 2^31.  Rows of q that belong to no
+ * request are not read and their outputs not written.  A position whose block
+ * lies outside the table or the cache is skipped and flagged.  What the cache
+ * holds behind a request's length never reaches a result; a NaN in a value row
+ * within it reaches every token of the request that shares a tile with one
+ * that sees it.
+ */
+int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t total_q,
+                                    int h_q, const smla_q8_cache* cache, const int32_t* block_table, int max_blocks,
+                                    int batch, const int32_t* cache_seqlens, const int32_t* cu_seqlens_q, int s_q,
+                                    int max_seqlen_q, int causal, float softmax_scale, float softcap,
+                                    const float* alibi_slopes, const int32_t* prefix_lens, const int32_t* doc_bounds,
+                                    void* o, float* lse, void* workspace, size_t workspace_bytes, uint32_t* status,
+                                    void* stream);
+
 /* Clear the workspace status word (asynchronously, on `stream`). */
 int smla_reset_device_status(void* workspace, void* stream);
 

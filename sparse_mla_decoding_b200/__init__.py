@@ -40,6 +40,15 @@ class SmlaError(RuntimeError):
         self.status = status
 
 
+class _Q8Cache(ctypes.Structure):
+    """smla_q8_cache."""
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("k_block_stride", ctypes.c_int64),
+                ("v_block_stride", ctypes.c_int64), ("k_scale_stride", ctypes.c_int64),
+                ("v_scale_stride", ctypes.c_int64), ("h_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("format", ctypes.c_int)]
+
+
 def lib() -> ctypes.CDLL:
     """Load libsmla.so (building it with nvcc first if it is missing or stale)."""
     global _lib
@@ -78,6 +87,17 @@ def lib() -> ctypes.CDLL:
             L.smla_sparse_fwd_workspace_bytes.restype = sz
             L.smla_quantize_kv.argtypes = [vp, vp, i64, vp, vp, i64, vp]
             L.smla_quantize_kv.restype = i32
+            L.smla_extend_block_table.argtypes = [vp, i32, vp, vp, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp]
+            L.smla_extend_block_table.restype = i32
+            L.smla_quantize_kv_blocks.argtypes = [vp, vp, i64, i64, i64, i64, i64, ctypes.POINTER(_Q8Cache), vp, i32,
+                                                  i32, vp, vp, vp, vp, vp]
+            L.smla_quantize_kv_blocks.restype = i32
+            L.smla_gqa_workspace_bytes.argtypes = [i32, i32]
+            L.smla_gqa_workspace_bytes.restype = sz
+            L.smla_gqa_attention_with_kvcache.argtypes = [vp, i64, i64, i64, i32, ctypes.POINTER(_Q8Cache), vp, i32,
+                                                          i32, vp, vp, i32, i32, i32, f32, f32, vp, vp, vp, vp, vp,
+                                                          vp, sz, vp, vp]
+            L.smla_gqa_attention_with_kvcache.restype = i32
             L.smla_get_device_status.argtypes = [vp, ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_uint32), vp]
             L.smla_get_device_status.restype = i32
             L.smla_reset_device_status.argtypes = [vp, vp]
@@ -458,6 +478,280 @@ def quantize_kv(latent: torch.Tensor, rope: torch.Tensor, kvcache: torch.Tensor,
     rc = lib().smla_quantize_kv(_ptr(latent), _ptr(rope), latent.shape[0], _ptr(slot_mapping), _ptr(kvcache),
                                 num_rows, _stream(latent.device))
     _check(rc, "smla_quantize_kv")
+
+
+# ---------------------------------------------------------------------------
+# paged serving of grouped-query attention: block tables, the block-scaled 8-bit
+# cache and attention over it
+# ---------------------------------------------------------------------------
+_paged_words: dict = {}
+
+
+def _paged_word(dev: torch.device) -> Optional[torch.Tensor]:
+    """The status word that the paged calls on a device share when they get no workspace.
+
+    Made by the first such call; a graph captured before that reports nowhere
+    (an allocation inside the capture would belong to the graph)."""
+    with _ws_lock:
+        w = _paged_words.get(dev.index)
+        if w is None and not torch.cuda.is_current_stream_capturing():
+            w = torch.zeros(64, dtype=torch.int32, device=dev)
+            torch.cuda.current_stream(dev).synchronize()    # other streams may use it next
+            _paged_words[dev.index] = w
+    return w
+
+
+def _paged_key(device: Optional[torch.device]) -> int:
+    dev = torch.device("cuda") if device is None else torch.device(device)
+    return dev.index if dev.index is not None else torch.cuda.current_device()
+
+
+def paged_status(device: Optional[torch.device] = None) -> Tuple[int, int]:
+    """(status, raw flags) of quantize_kv_blocks and gqa_attention_with_kvcache calls on
+    `device` that were given no workspace (see STATUS_FLAGS; sticky until
+    reset_paged_status).  Synchronises the current stream; (0, 0) before any such call."""
+    with _ws_lock:
+        w = _paged_words.get(_paged_key(device))
+    return (0, 0) if w is None else get_device_status(w)
+
+
+def reset_paged_status(device: Optional[torch.device] = None) -> None:
+    """Clear the status word that paged_status reads (on the current stream)."""
+    with _ws_lock:
+        w = _paged_words.get(_paged_key(device))
+    if w is not None:
+        reset_device_status(w)
+
+
+def _i32_vector(t: torch.Tensor, n: int, name: str, dev: torch.device) -> torch.Tensor:
+    _require(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and tuple(t.shape) == (n,) and t.device == dev,
+             f"{name} must be int32 [{n}] on {dev}")
+    return t.contiguous()
+
+
+def _block_table(t: torch.Tensor, b: int, dev: torch.device) -> None:
+    _require(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.dim() == 2 and t.shape[0] == b and
+             t.shape[1] >= 1 and t.device == dev and t.is_contiguous(),
+             f"block_table must be contiguous int32 [{b}, max_blocks] on {dev}")
+
+
+def extend_block_table(block_table: torch.Tensor, cache_seqlens: torch.Tensor, new_lens: torch.Tensor,
+                       free_blocks: torch.Tensor, num_free: torch.Tensor, max_new_tokens: int
+                       ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Blocks and cache rows for the new tokens of a step, without a host copy of the lengths.
+
+    block_table: int32 [b, max_blocks], fresh entries written in place;
+    cache_seqlens, new_lens: int32 [b], tokens held and tokens to add;
+    free_blocks: int32 [capacity] whose first num_free (int32 [1]) entries are free,
+    taken from the end; max_new_tokens: length of the slot map.
+    Returns (slot_mapping int64 [max_new_tokens], cu_new int32 [b + 1], the lengths with
+    the new tokens int32 [b], entries left on the free list int32 [1]).  A request whose
+    blocks or tokens do not fit keeps its length, and its tokens get slots -1, which
+    quantize_kv skips.  slot_mapping goes to quantize_kv; cu_new and the lengths go to
+    quantize_kv_blocks and the attention calls.
+    """
+    _require(isinstance(block_table, torch.Tensor) and block_table.is_cuda and block_table.dim() == 2,
+             "block_table must be int32 [b, max_blocks] on CUDA")
+    dev, b = block_table.device, block_table.shape[0]
+    _block_table(block_table, b, dev)
+    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", dev)
+    new_lens = _i32_vector(new_lens, b, "new_lens", dev)
+    num_free = _i32_vector(num_free, 1, "num_free", dev)
+    _require(free_blocks.dtype == torch.int32 and free_blocks.dim() == 1 and free_blocks.device == dev,
+             f"free_blocks must be int32 [capacity] on {dev}")
+    free_blocks = free_blocks.contiguous()
+    n = int(max_new_tokens)
+    _require(0 <= n < 1 << 31, "max_new_tokens must be in [0, 2^31)")
+    slots = torch.empty(n, dtype=torch.int64, device=dev)
+    cu_new = torch.empty(b + 1, dtype=torch.int32, device=dev)
+    lens = torch.empty(b, dtype=torch.int32, device=dev)
+    left = torch.empty(1, dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        rc = lib().smla_extend_block_table(_ptr(block_table), block_table.shape[1], _ptr(cache_seqlens),
+                                           _ptr(new_lens), b, _ptr(free_blocks), free_blocks.numel(), _ptr(num_free),
+                                           n, _ptr(slots), _ptr(cu_new), _ptr(lens), _ptr(left), _stream(dev))
+    _check(rc, "smla_extend_block_table")
+    return slots, cu_new, lens, left
+
+
+_Q8_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
+
+def _q8_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor) -> _Q8Cache:
+    _require(isinstance(k_cache, torch.Tensor) and k_cache.is_cuda and k_cache.dim() == 4 and
+             k_cache.dtype in _Q8_FORMATS and k_cache.shape[2] == BLOCK_SIZE and k_cache.shape[3] in (64, 128),
+             "k_cache must be e4m3 or int8 [num_blocks, h_kv, 64, 64 or 128] on CUDA")
+    nb, h_kv, _, d = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _require(t.dtype == k_cache.dtype and t.shape == k_cache.shape and t.device == k_cache.device,
+                 f"{name} must match k_cache's type, shape and device")
+        _require((h_kv == 1 or t.stride(1) == BLOCK_SIZE * d) and t.stride(2) == d and t.stride(3) == 1,
+                 f"{name} must be dense within a block")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _require(t.dtype == torch.float32 and tuple(t.shape) == (nb, h_kv) and t.device == k_cache.device and
+                 (h_kv == 1 or t.stride(1) == 1), f"{name} must be float32 [num_blocks, h_kv] on {k_cache.device}")
+    block = h_kv * BLOCK_SIZE * d     # a lone block's stride is free to say anything
+    return _Q8Cache(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb,
+                    k_cache.stride(0) if nb > 1 else block, v_cache.stride(0) if nb > 1 else block,
+                    k_scale.stride(0) if nb > 1 else h_kv, v_scale.stride(0) if nb > 1 else h_kv, h_kv, d,
+                    _Q8_FORMATS[k_cache.dtype])
+
+
+def _rows16(t: torch.Tensor) -> torch.Tensor:
+    """t [n, h, d] with dense rows that 16-byte loads can read; a copy where it has none."""
+    ok = t.stride(2) == 1 and t.stride(0) % 8 == 0 and t.stride(1) % 8 == 0 and t.data_ptr() % 16 == 0
+    return t if ok else t.contiguous()
+
+
+def quantize_kv_blocks(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                       cache_seqlens: torch.Tensor, new_seqlens: torch.Tensor, cu_new: torch.Tensor,
+                       check_device_status: bool = False) -> None:
+    """Write new tokens into a block-scaled 8-bit cache.
+
+    k, v: bf16 [total, h_kv, d], the tokens cu_new[r] .. cu_new[r + 1] - 1 of request r
+    (strided views of a fused projection are read in place); k_cache, v_cache: e4m3
+    (torch.float8_e4m3fn) or int8 [num_blocks, h_kv, 64, d], dense within a block;
+    k_scale, v_scale: float32 [num_blocks, h_kv]; block_table: int32 [b, max_blocks];
+    cache_seqlens, new_seqlens: int32 [b], the lengths before and with the tokens;
+    cu_new: int32 [b + 1].  A (block, head)'s scale is the smallest power of two at which
+    its values fit the code range, and never shrinks while the block fills: where new
+    tokens raise it, the block's older codes are rescaled.  A request whose lengths do
+    not differ by its token count (extend_block_table found no room) is left alone.  No
+    two requests may write to the same block.  Problems found on the device are flagged:
+    paged_status(), or check_device_status=True to synchronise and raise.
+    """
+    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    for name, t in (("k", k), ("v", v)):
+        _require(t.dtype == torch.bfloat16 and t.dim() == 3 and tuple(t.shape[1:]) == (cache.h_kv, cache.head_dim) and
+                 t.shape[0] == k.shape[0] and t.device == dev,
+                 f"{name} must be bf16 [total, {cache.h_kv}, {cache.head_dim}] on {dev}")
+    b = block_table.shape[0]
+    _block_table(block_table, b, dev)
+    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", dev)
+    new_seqlens = _i32_vector(new_seqlens, b, "new_seqlens", dev)
+    cu_new = _i32_vector(cu_new, b + 1, "cu_new", dev)
+    k, v = _rows16(k), _rows16(v)
+    with torch.cuda.device(dev):
+        word = _paged_word(dev)
+        rc = lib().smla_quantize_kv_blocks(_ptr(k), _ptr(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                                           k.shape[0], ctypes.byref(cache), _ptr(block_table), block_table.shape[1],
+                                           b, _ptr(cache_seqlens), _ptr(new_seqlens), _ptr(cu_new), _ptr(word),
+                                           _stream(dev))
+    _check(rc, "smla_quantize_kv_blocks")
+    if check_device_status and word is not None:
+        _raise_on_flags(word, "smla_quantize_kv_blocks")
+
+
+def gqa_workspace_bytes(head_dim: int, device: Optional[torch.device] = None) -> int:
+    n = lib().smla_gqa_workspace_bytes(int(head_dim), _paged_key(device))
+    if n == 0:
+        raise SmlaError(1, "smla_gqa_workspace_bytes")
+    return int(n)
+
+
+def new_gqa_workspace(head_dim: int, device: Optional[torch.device] = None) -> torch.Tensor:
+    """A workspace for gqa_attention_with_kvcache: a zeroed 256-byte header (the device
+    status word), then the split partials."""
+    return torch.zeros(256 + gqa_workspace_bytes(head_dim, device), dtype=torch.uint8,
+                       device=torch.device("cuda", _paged_key(device)))
+
+
+def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                               v_scale: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                               cu_seqlens_q: Optional[torch.Tensor] = None, max_seqlen_q: Optional[int] = None,
+                               causal: bool = True, softmax_scale: Optional[float] = None, softcap: float = 0.0,
+                               alibi_slopes: Optional[torch.Tensor] = None,
+                               prefix_lens: Optional[torch.Tensor] = None,
+                               doc_bounds: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None,
+                               out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                               check_device_status: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Grouped-query attention over a block-scaled 8-bit cache (see quantize_kv_blocks).
+
+    q: bf16 [b, s_q, h_q, d], or [total_q, h_q, d] with cu_seqlens_q int32 [b + 1]; a
+    request's query tokens are its last positions and are already in the cache, so
+    cache_seqlens (int32 [b]) counts them.  One new token per request, several, or whole
+    prompts: max_seqlen_q (the most query tokens of a request; total_q if not given) only
+    picks the kernel.
+    Scores are softmax_scale * <q, k> (default 1/sqrt(d)), then softcap * tanh(x / softcap)
+    with softcap > 0, then minus alibi_slopes[h] * distance (float32 [h_q]).
+    A token at position p sees j <= p (causal), every j < prefix_lens[r] as well (int32
+    [b]), and with doc_bounds (int32 [total_q, 2]) only first <= j < end of its own
+    document.  Returns (o bf16 as q, lse float32 [b, s_q, h_q] or [total_q, h_q]); 0 and
+    -inf where a token sees nothing.  Rows of q behind the last request are not read and
+    their outputs not written.
+    A workspace from new_gqa_workspace may be passed; its first 256 bytes are the device
+    status word.  Without one, scratch comes from torch's allocator (a captured graph
+    keeps its own) and flags go to paged_status().
+    """
+    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    _require(isinstance(q, torch.Tensor) and q.dtype == torch.bfloat16 and q.device == dev and
+             q.dim() == (4 if cu_seqlens_q is None else 3) and q.shape[-1] == cache.head_dim,
+             f"q must be bf16 [b, s_q, h_q, {cache.head_dim}], or [total_q, h_q, {cache.head_dim}] with cu_seqlens_q, "
+             f"on {dev}")
+    b = block_table.shape[0]
+    _block_table(block_table, b, dev)
+    h_q = q.shape[-2]
+    _require(h_q >= 1 and h_q % cache.h_kv == 0, "h_q must be a multiple of h_kv")
+    shape = q.shape
+    s_q = 0
+    if cu_seqlens_q is None:
+        _require(q.shape[0] == b, f"q must hold {b} requests")
+        s_q = q.shape[1]
+        if max_seqlen_q is None:
+            max_seqlen_q = s_q
+        q = q.flatten(0, 1)
+    else:
+        cu_seqlens_q = _i32_vector(cu_seqlens_q, b + 1, "cu_seqlens_q", dev)
+    q = _rows16(q)
+    total = q.shape[0]
+    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", dev)
+    if alibi_slopes is not None:
+        _require(alibi_slopes.dtype == torch.float32 and tuple(alibi_slopes.shape) == (h_q,) and
+                 alibi_slopes.device == dev, f"alibi_slopes must be float32 [{h_q}] on {dev}")
+        alibi_slopes = alibi_slopes.contiguous()
+    if prefix_lens is not None:
+        _require(causal, "prefix_lens needs causal=True")
+        prefix_lens = _i32_vector(prefix_lens, b, "prefix_lens", dev)
+    if doc_bounds is not None:
+        _require(doc_bounds.dtype == torch.int32 and tuple(doc_bounds.shape) == (total, 2) and
+                 doc_bounds.device == dev, f"doc_bounds must be int32 [{total}, 2] on {dev}")
+        doc_bounds = doc_bounds.contiguous()
+        if doc_bounds.data_ptr() % 8:
+            doc_bounds = doc_bounds.clone()
+    softcap = float(softcap)
+    _require(0.0 <= softcap < math.inf, "softcap must be >= 0 and finite")
+    scale = -1.0 if softmax_scale is None else float(softmax_scale)
+    _require(softmax_scale is None or 0.0 < scale < math.inf, "softmax_scale must be > 0 and finite")
+    if out is None:
+        o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    else:
+        o, lse = out
+        for name, t, dt, sh in (("o", o, torch.bfloat16, shape), ("lse", lse, torch.float32, shape[:-1])):
+            _require(t.dtype == dt and t.shape == sh and t.device == dev and t.is_contiguous(),
+                     f"out: {name} must be contiguous {dt} {list(sh)} on {dev}")
+    with torch.cuda.device(dev):
+        nbytes = gqa_workspace_bytes(cache.head_dim, dev)
+        if workspace is None:
+            word, scratch = _paged_word(dev), torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        else:
+            _require(workspace.device == dev and workspace.is_contiguous() and workspace.dtype == torch.uint8 and
+                     workspace.numel() >= 256 + nbytes, f"workspace needs {256 + nbytes} bytes of uint8 on {dev}")
+            word, scratch = workspace[:256], workspace[256:]
+        rc = lib().smla_gqa_attention_with_kvcache(
+            _ptr(q), q.stride(0), q.stride(1), total, h_q, ctypes.byref(cache), _ptr(block_table),
+            block_table.shape[1], b, _ptr(cache_seqlens), _ptr(cu_seqlens_q), s_q,
+            total if max_seqlen_q is None else int(max_seqlen_q), 1 if causal else 0, scale, softcap,
+            _ptr(alibi_slopes), _ptr(prefix_lens), _ptr(doc_bounds), _ptr(o), _ptr(lse), _ptr(scratch),
+            scratch.numel(), _ptr(word), _stream(dev))
+    _check(rc, "smla_gqa_attention_with_kvcache")
+    if check_device_status and word is not None:
+        _raise_on_flags(word, "smla_gqa_attention_with_kvcache")
+    return o, lse
 
 
 def get_device_status(workspace: torch.Tensor) -> Tuple[int, int]:

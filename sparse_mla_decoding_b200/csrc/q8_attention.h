@@ -1,0 +1,27 @@
+// q8_attention.h -- launch interface of the attention kernels over the
+// block-scaled 8-bit cache (internal).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "q8_cache.h"
+
+namespace smla {
+
+constexpr int kQ8DecodeWarps = 8;        // warps of a CTA, each with its own range of the work
+constexpr int64_t kQ8MinVisits = 2;      // least blocks of a warp's range
+
+// Partials of the decode kernel: two slots of 16 rows for each warp.
+struct Q8Scratch {
+  float* o;                              // [2 parts][16][d], normalised
+  float* lse;                            // [2 parts][16], log2
+  int32_t* meta;                         // [parts][8]: the unit a part begins inside
+};
+
+cudaError_t launch_q8_decode(const Q8Params& p, bool int8, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                             const Q8Scratch& scratch, int ctas, cudaStream_t stream);
+
+}  // namespace smla

@@ -1,0 +1,167 @@
+// q8_cache.h -- what the kernels over the block-scaled 8-bit cache share: the
+// launch parameters, the codes and their conversions, and the visibility rule.
+//
+// The cache holds keys and values in blocks of 64 tokens: codes
+// [num_blocks][h_kv][64][d] in e4m3 or int8 and one float32 scale for each
+// (block, head); a key is code * scale.  Row r of a request's n new tokens
+// stands at position len - n + t of the request.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace smla {
+
+constexpr int kBlk = 64;          // tokens per cache block
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Everything an attention call over the cache needs; offsets and strides in
+// elements unless they say bytes.
+struct Q8Params {
+  const __nv_bfloat16* q;         // [total_q][h_q][d]
+  int64_t q_token_stride, q_head_stride;
+  const float *k_scale, *v_scale; // [num_blocks][h_kv]
+  int64_t k_scale_stride, v_scale_stride;
+  const uint8_t *k_cache, *v_cache;
+  int64_t k_block_bytes, v_block_bytes;
+  int64_t num_blocks;
+  const int32_t* block_table;     // [batch][max_blocks]
+  const int32_t* seqlens;         // [batch], with the new tokens
+  const int32_t* cu_q;            // [batch + 1], or NULL: s_q tokens each
+  const float* slopes;            // [h_q] or NULL
+  const int32_t* prefix;          // [batch] or NULL
+  const int32_t* docs;            // [total_q][2] or NULL
+  int max_blocks, batch, s_q, total_q, h_q, h_kv, group, d;
+  int causal;
+  float scale;                    // softmax scale
+  float cap;                      // 0: none
+  __nv_bfloat16* o;               // [total_q][h_q][d]
+  float* lse;                     // [total_q][h_q]
+  uint32_t* status;               // may be NULL
+};
+
+// A request as the kernels see it.  n is 0 where the offsets are not usable.
+struct Q8Request {
+  int q0, n, len;                 // first row in q, new tokens, cache length
+  int prefix;
+};
+
+__device__ __forceinline__ Q8Request q8_request(const Q8Params& p, int r, bool* bad) {
+  Q8Request x;
+  if (p.cu_q) {
+    const int a = p.cu_q[r], b = p.cu_q[r + 1];
+    const bool ok = a >= 0 && b >= a && b <= p.total_q;
+    *bad = !ok;
+    x.q0 = ok ? a : 0;
+    x.n = ok ? b - a : 0;
+  } else {
+    *bad = false;
+    x.q0 = r * p.s_q;
+    x.n = p.s_q;
+  }
+  x.len = max(p.seqlens[r], 0);
+  x.prefix = p.prefix ? p.prefix[r] : 0;
+  return x;
+}
+
+// The cache positions [lo, hi) that new token t of a request sees.
+__device__ __forceinline__ void q8_visible(const Q8Params& p, const Q8Request& x, int t, int& lo, int& hi) {
+  lo = 0;
+  hi = x.len;
+  if (p.causal) hi = min(hi, max(x.len - x.n + t + 1, x.prefix));
+  if (p.docs) {
+    const int2 d = reinterpret_cast<const int2*>(p.docs)[x.q0 + t];
+    lo = max(d.x, 0);
+    hi = min(hi, d.y);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// codes -> f16: every e4m3 and int8 code is exact in f16 (4 and 8 significant
+// bits; e4m3's range 2^-9 .. 448 lies inside f16's), so the matrix products see
+// the cache's codes unrounded and the scales are applied in fp32.
+// ---------------------------------------------------------------------------
+template <bool kInt8>
+struct Q8Codes;
+
+template <>
+struct Q8Codes<false> {
+  // four codes of one word as two f16 pairs
+  static __device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+};
+
+template <>
+struct Q8Codes<true> {
+  // int8 + 128 as the low byte of 1024.0 (0x6400), then minus 1152: exact.
+  static __device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    w ^= 0x80808080u;
+    lo = __byte_perm(w, 0x64646464u, 0x4140);
+    hi = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), off);
+    __half2 b = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
+    lo = *reinterpret_cast<uint32_t*>(&a);
+    hi = *reinterpret_cast<uint32_t*>(&b);
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The power of two that brings a row maximum `amax` into [1, 2) (as far as
+// fp32's exponents reach), and its inverse.
+__device__ __forceinline__ void row_pow2(float amax, float& up, float& down) {
+  const int e = (int)(__float_as_uint(amax) >> 23) & 0xFF;
+  const int k = min(max(e, 1), 253);
+  up = __uint_as_float((uint32_t)(254 - k) << 23);
+  down = __uint_as_float((uint32_t)k << 23);
+}
+
+// tanh for score caps.  |x| <= 0.75: x P(x^2), P a degree-5 fit to tanh(x)/x in
+// relative error (1.6e-7 in fp32, fitted by reweighted least squares on
+// Chebyshev nodes), so a small score keeps its relative precision; larger |x|:
+// 1 - 2 / (1 + exp(2|x|)) with the sign of x.
+__device__ __forceinline__ float tanh_small(float x) {
+  const float z = x * x;
+  float r = -0.004716585855931044f;
+  r = fmaf(r, z, 0.01958341710269451f);
+  r = fmaf(r, z, -0.0533447191119194f);
+  r = fmaf(r, z, 0.13325412571430206f);
+  r = fmaf(r, z, -0.33332958817481995f);
+  r = fmaf(r, z, 1.0f);
+  return r * x;
+}
+__device__ __forceinline__ float tanh_full(float x) {
+  const float a = fabsf(x);
+  float rc;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(rc) : "f"(1.f + ex2(a * (2.f * kLog2e))));
+  const float big = copysignf(fmaf(-2.f, rc, 1.f), x);
+  return a <= 0.75f ? tanh_small(x) : big;
+}
+
+// log2 of a value scale relative to `base`, kept within 2^+-60 (a zero scale
+// has only zero codes behind it, so any value does; the clamp keeps the
+// softmax denominator inside fp32).
+__device__ __forceinline__ float rel_log2(float scale, float base_log2) {
+  return fminf(fmaxf(log2f(scale) - base_log2, -60.f), 60.f);
+}
+
+}  // namespace smla

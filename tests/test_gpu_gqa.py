@@ -1,0 +1,290 @@
+"""Grouped-query attention over the block-scaled 8-bit cache on the GPU against the
+definition in float64: head groups, lengths around the blocks' edges, one and many
+new tokens, capped and biased scores, masks that leave rows empty, split schedules."""
+import numpy as np
+import pytest
+import torch
+
+import paged_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+def build(q_lens, lens, h_q, h_kv, d, kind, seed, poison=True):
+    """Inputs on the host; rows behind a request's length and blocks of no request hold NaN (e4m3)."""
+    lens, q_lens = np.asarray(lens, np.int32), np.asarray(q_lens, np.int32)
+    table, blocks = U.make_table(lens, seed)
+    kc, ks, k = U.make_cache(blocks, h_kv, d, kind, seed + 1)
+    vc, vs, v = U.make_cache(blocks, h_kv, d, kind, seed + 2)
+    if poison:
+        dead = np.ones((blocks, U.BLOCK), bool)
+        for r, n in enumerate(lens):
+            for b in range(-(-int(n) // U.BLOCK)):
+                dead[table[r, b], :min(U.BLOCK, int(n) - b * U.BLOCK)] = False
+        mask = torch.from_numpy(dead)[:, None, :, None].expand(kc.shape)
+        for c in (kc, vc):
+            c.view(torch.int8)[mask] = 127      # NaN in e4m3
+    g = torch.Generator().manual_seed(seed + 3)
+    cu = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    q = (torch.randn(int(cu[-1]), h_q, d, generator=g) * 1.5).to(torch.bfloat16)
+    return dict(q=q, kc=kc, vc=vc, ks=ks, vs=vs, table=table, lens=lens, cu=cu, k=k, v=v)
+
+
+def call(x, four_d=None, **kw):
+    import sparse_mla_decoding_b200 as smla
+    dev = {n: x[n].cuda() if isinstance(x[n], torch.Tensor) else torch.from_numpy(x[n]).cuda()
+           for n in ("q", "kc", "vc", "ks", "vs", "table", "lens", "cu")}
+    gpu = {n: torch.from_numpy(np.asarray(a)).cuda() if isinstance(a, np.ndarray) else a for n, a in kw.items()}
+    ws = smla.new_gqa_workspace(dev["kc"].shape[3])
+    q, cu = (dev["q"], dev["cu"]) if four_d is None else (dev["q"].view(four_d), None)
+    o, lse = smla.gqa_attention_with_kvcache(q, dev["kc"], dev["vc"], dev["ks"], dev["vs"], dev["table"], dev["lens"],
+                                             cu_seqlens_q=cu, workspace=ws, **gpu)
+    torch.cuda.synchronize()
+    return o, lse, smla.get_device_status(ws)
+
+
+def reference(x, **kw):
+    names = {"alibi_slopes": "slopes", "prefix_lens": "prefix", "doc_bounds": "docs", "softmax_scale": "scale"}
+    kw = {names.get(n, n): a for n, a in kw.items() if n != "max_seqlen_q"}
+    return U.attention(x["q"].double().numpy(), x["k"], x["v"], x["table"], x["lens"], x["cu"],
+                       v_scale=x["vs"].double().numpy(), **kw)
+
+
+def check(x, **kw):
+    o, lse, (status, raw) = call(x, **kw)
+    assert status == 0, f"flags {raw:#x}"
+    U.compare(o, lse, reference(x, **kw))
+    return o, lse
+
+
+KINDS = ["e4m3", "int8"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h_q,h_kv", [(8, 8), (8, 1), (14, 2), (5, 5), (32, 1)])
+def test_single_tokens(h_q, h_kv, d, kind):
+    """Lengths of one token, around a block's and a tile's edge, and over several blocks."""
+    x = build([1] * 8, [1, 2, 63, 64, 65, 129, 500, 17], h_q, h_kv, d, kind, 100 + d + h_q)
+    check(x)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_several_tokens_and_empty_requests(d, kind):
+    """Requests without new tokens, without a cache, with more new tokens than one row tile holds."""
+    x = build([3, 0, 1, 7, 0, 70, 2], [300, 5, 1, 7, 0, 200, 64], 12, 4, d, kind, 200 + d)
+    check(x)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_new_tokens_than_cache(d):
+    """Tokens before the start of the cache see nothing."""
+    x = build([5, 4], [2, 0], 4, 2, d, "e4m3", 250 + d)
+    o, lse = check(x)
+    assert torch.isinf(lse[:3]).all() and torch.isinf(lse[5:]).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("mods", ["cap", "cap_small", "alibi", "cap+alibi", "full", "full+alibi"])
+def test_scores(mods, kind):
+    x = build([1, 4, 40, 1], [400, 129, 130, 3], 16, 2, 128, kind, 300)
+    kw = {}
+    if "cap" in mods:
+        kw["softcap"] = 0.8 if "small" in mods else 30.0
+    if "alibi" in mods:
+        kw["alibi_slopes"] = np.exp2(-np.arange(16) / 2).astype(np.float32)
+    if "full" in mods:
+        kw["causal"] = False
+    check(x, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix(d):
+    """A prefix longer than the causal reach, shorter, zero, and past the end of the cache."""
+    x = build([20, 20, 1, 33], [20, 150, 100, 70], 8, 4, d, "int8", 400 + d)
+    check(x, prefix_lens=np.array([9, 140, 0, 5000], np.int32))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_documents(d, causal):
+    """Documents that start inside a block, that hold one token, that end before their token and that are empty."""
+    x = build([1, 6, 50, 1], [700, 70, 300, 40], 8, 2, d, "e4m3", 500 + d)
+    docs = [(650, 700)] + [(64, 65), (65, 70), (0, 64), (66, 66), (30, 1000), (-5, 3)]
+    docs += [(200, 290)] * 30 + [(290, 300)] * 20 + [(20, 10)]
+    o, lse = check(x, doc_bounds=np.array(docs, np.int32), causal=causal)
+    assert torch.isinf(lse[-1]).all() and (o[-1] == 0).all()
+
+
+def test_prefix_and_documents_and_bias_together():
+    x = build([40, 3], [200, 90], 6, 2, 128, "e4m3", 550)
+    docs = np.array([(0, 180)] * 20 + [(180, 200)] * 20 + [(10, 90)] * 3, np.int32)
+    check(x, doc_bounds=docs, prefix_lens=np.array([100, 0], np.int32), softcap=20.0,
+          alibi_slopes=np.full(6, 0.05, np.float32), softmax_scale=0.11)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_split_over_many_warps(kind):
+    """One long request: its blocks are spread over many warps and merged."""
+    x = build([1, 2], [20011, 1500], 8, 2, 128, kind, 600)
+    check(x)
+
+
+def test_many_short_requests():
+    """More requests than a CTA has threads, each shorter than a block or two."""
+    rng = np.random.default_rng(7)
+    lens = rng.integers(0, 100, 700)
+    x = build(np.minimum(1, lens), lens, 4, 2, 64, "int8", 700)
+    check(x)
+
+
+def test_four_dimensional_queries_equal_packed_ones():
+    x = build([3] * 5, [3, 64, 100, 259, 30], 8, 4, 128, "e4m3", 800)
+    o, lse, _ = call(x)
+    o4, lse4, _ = call(x, four_d=(5, 3, 8, 128))
+    assert torch.equal(o.view(5, 3, 8, 128), o4) and torch.equal(lse.view(5, 3, 8), lse4)
+
+
+@pytest.mark.parametrize("hint", [1, 4, 100000])
+def test_hint_changes_nothing_that_is_computed(hint):
+    x = build([1, 30, 2], [100, 90, 300], 8, 2, 128, "e4m3", 850)
+    check(x, max_seqlen_q=hint)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_zero_scales_and_large_spreads(n):
+    """Blocks of zero keys or values beside ordinary ones, and scales far apart."""
+    x = build([n], [400], 8, 2, 128, "int8", 900, poison=False)
+    blocks = x["table"][0, :7]
+    x["vs"][blocks[1]] = 0
+    x["vs"][blocks[3]] *= 2.0 ** 30
+    x["vs"][blocks[4]] *= 2.0 ** -25
+    x["ks"][blocks[2]] = 0
+    for codes, scale, name in (("kc", "ks", "k"), ("vc", "vs", "v")):
+        x[name] = x[codes].double().numpy() * x[scale].double().numpy()[:, :, None, None]
+    check(x)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e30])
+def test_far_query_sizes(size):
+    """Queries far outside f16's range: scores of ordinary size come from the softmax scale."""
+    x = build([2], [90], 4, 2, 64, "e4m3", 950)
+    x["q"] = (x["q"].double() * size).to(torch.bfloat16)
+    check(x, softmax_scale=float(0.125 / size))
+
+
+def test_strided_queries_scales_and_blocks():
+    """Query rows inside a fused projection; keys and values in one allocation."""
+    import sparse_mla_decoding_b200 as smla
+    x = build([2, 1], [100, 257], 8, 2, 128, "e4m3", 1000)
+    nb = x["kc"].shape[0]
+    both = torch.zeros(nb, 2, 2, 64, 128, dtype=torch.int8, device="cuda")
+    both[:, 0], both[:, 1] = x["kc"].view(torch.int8).cuda(), x["vc"].view(torch.int8).cuda()
+    both = both.view(torch.float8_e4m3fn)
+    scales = torch.stack([x["ks"], x["vs"]], 1).cuda()
+    fused = torch.full((3, 12, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fused[:, 2:10] = x["q"].cuda()
+    args = [torch.from_numpy(x[n]).cuda() for n in ("table", "lens")]
+    o, lse = smla.gqa_attention_with_kvcache(fused[:, 2:10], both[:, 0], both[:, 1], scales[:, 0], scales[:, 1], *args,
+                                             cu_seqlens_q=torch.from_numpy(x["cu"]).cuda(), check_device_status=True)
+    U.compare(o, lse, reference(x))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_rows_behind_the_last_request_are_left(n):
+    import sparse_mla_decoding_b200 as smla
+    x = build([n, n], [100, 70], 8, 2, 128, "e4m3", 1100)
+    q = torch.cat([x["q"], torch.full((7, 8, 128), float("nan"), dtype=torch.bfloat16)]).cuda()
+    o = torch.full((2 * n + 7, 8, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((2 * n + 7, 8), 5.0, device="cuda")
+    smla.gqa_attention_with_kvcache(q, x["kc"].cuda(), x["vc"].cuda(), x["ks"].cuda(), x["vs"].cuda(),
+                                    *(torch.from_numpy(x[k]).cuda() for k in ("table", "lens", "cu")), out=(o, lse))
+    U.compare(o[:2 * n], lse[:2 * n], reference(x))
+    assert (o[2 * n:] == 3).all() and (lse[2 * n:] == 5).all()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_bad_blocks_are_skipped_and_flagged(n):
+    x = build([n], [300], 8, 2, 128, "e4m3", 1200)
+    x["table"][0, 1] = -7
+    x["table"][0, 3] = x["kc"].shape[0]
+    o, lse, (status, raw) = call(x)
+    assert status == 1 and raw == 2
+    U.compare(o, lse, reference(x))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_length_past_the_table_is_flagged(n):
+    x = build([n], [128], 4, 2, 64, "int8", 1250)
+    x["table"] = np.ascontiguousarray(x["table"][:, :2])
+    x["lens"] = np.array([1000], np.int32)
+    o, lse, (status, raw) = call(x, causal=False)
+    assert status == 1 and raw == 2
+    x["table"] = np.concatenate([x["table"], np.full((1, 20), -1, np.int32)], 1)
+    U.compare(o, lse, reference(x, causal=False))
+
+
+def test_bad_offsets_are_flagged_and_leave_the_others():
+    x = build([2, 3, 2], [100, 80, 90], 4, 2, 64, "e4m3", 1300)
+    ref = reference(x)
+    x["cu"] = np.array([0, 2, 1, 7], np.int32)      # request 1 runs backwards, request 2 claims rows 1 .. 6
+    o, lse, (status, raw) = call(x)
+    assert status == 1 and raw & 4
+    U.compare(o[:1], lse[:1], [a[:1] for a in ref])
+
+
+def test_repeated_calls_are_bitwise_equal():
+    x = build([1, 2, 30], [5000, 900, 300], 16, 2, 128, "e4m3", 1400)
+    first = call(x)
+    for _ in range(10):
+        again = call(x)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_a_captured_call_replays_on_new_inputs():
+    """A graph keeps its own scratch: replays beside eager calls, on another stream, give the eager results."""
+    import sparse_mla_decoding_b200 as smla
+    x = build([1, 2, 30], [3000, 900, 300], 16, 2, 128, "e4m3", 1500)
+    t = {n: (x[n] if isinstance(x[n], torch.Tensor) else torch.from_numpy(x[n])).cuda()
+         for n in ("q", "kc", "vc", "ks", "vs", "table", "lens", "cu")}
+
+    def run():
+        return smla.gqa_attention_with_kvcache(t["q"], t["kc"], t["vc"], t["ks"], t["vs"], t["table"], t["lens"],
+                                               cu_seqlens_q=t["cu"])
+    run()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        o, lse = run()
+    q2 = t["q"].flip(0).contiguous()
+    t["q"].copy_(q2)
+    t["lens"].copy_(torch.tensor([1000, 890, 200], dtype=torch.int32))
+    torch.cuda.synchronize()
+    other = run()
+    with torch.cuda.stream(side):
+        graph.replay()
+    beside = [run() for _ in range(3)]
+    torch.cuda.synchronize()
+    for a in [other] + beside:
+        assert torch.equal(a[0], o) and torch.equal(a[1], lse)
+    assert smla.paged_status()[0] == 0
+
+
+def test_two_streams_at_once():
+    import sparse_mla_decoding_b200 as smla
+    xs = [build([1, 1], [4000, 70], 8, 2, 128, kind, 1600) for kind in KINDS]
+    ts = [{n: (x[n] if isinstance(x[n], torch.Tensor) else torch.from_numpy(x[n])).cuda()
+           for n in ("q", "kc", "vc", "ks", "vs", "table", "lens", "cu")} for x in xs]
+    streams = [torch.cuda.Stream() for _ in ts]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, (t, s) in enumerate(zip(ts, streams)):
+            with torch.cuda.stream(s):
+                outs[i].append(smla.gqa_attention_with_kvcache(t["q"], t["kc"], t["vc"], t["ks"], t["vs"], t["table"],
+                                                               t["lens"], cu_seqlens_q=t["cu"]))
+    torch.cuda.synchronize()
+    for x, got in zip(xs, outs):
+        U.compare(*got[0], reference(x))
+        assert all(torch.equal(a[0], got[0][0]) and torch.equal(a[1], got[0][1]) for a in got)
