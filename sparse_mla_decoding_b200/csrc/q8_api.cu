@@ -176,9 +176,6 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   const Layout wl = workspace(cache->head_dim, sms);
   if (workspace_bytes < wl.total) return SMLA_ERR_INVALID_ARGUMENT;
 
-  CUtensorMap k_map, v_map;
-  if (int rc = tile_map(&k_map, cache->k_cache, cache, cache->k_block_stride)) return rc;
-  if (int rc = tile_map(&v_map, cache->v_cache, cache, cache->v_block_stride)) return rc;
   smla::Q8Params p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_token_stride = q_token_stride;
@@ -212,12 +209,20 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.status = status;
+  const bool int8 = cache->format == SMLA_Q8_INT8;
+  if ((int64_t)max_seqlen_q * p.group > smla::kQ8DecodeRows) {
+    const cudaError_t e = smla::launch_q8_prefill(p, int8, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SMLA_OK : smla::cuda_failure(e);
+  }
+  CUtensorMap k_map, v_map;
+  if (int rc = tile_map(&k_map, cache->k_cache, cache, cache->k_block_stride)) return rc;
+  if (int rc = tile_map(&v_map, cache->v_cache, cache, cache->v_block_stride)) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace_ptr);
   smla::Q8Scratch scratch;
   scratch.o = reinterpret_cast<float*>(ws);
   scratch.lse = reinterpret_cast<float*>(ws + wl.lse_off);
   scratch.meta = reinterpret_cast<int32_t*>(ws + wl.meta_off);
-  const cudaError_t e = smla::launch_q8_decode(p, cache->format == SMLA_Q8_INT8, k_map, v_map, scratch, sms,
+  const cudaError_t e = smla::launch_q8_decode(p, int8, k_map, v_map, scratch, sms,
                                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SMLA_OK : smla::cuda_failure(e);
 }
