@@ -119,6 +119,11 @@ def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream of device `index` as a cudaStream_t, without the Stream object."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -492,12 +497,14 @@ def _paged_word(dev: torch.device) -> Optional[torch.Tensor]:
 
     Made by the first such call; a graph captured before that reports nowhere
     (an allocation inside the capture would belong to the graph)."""
-    with _ws_lock:
-        w = _paged_words.get(dev.index)
-        if w is None and not torch.cuda.is_current_stream_capturing():
-            w = torch.zeros(64, dtype=torch.int32, device=dev)
-            torch.cuda.current_stream(dev).synchronize()    # other streams may use it next
-            _paged_words[dev.index] = w
+    w = _paged_words.get(dev.index)
+    if w is None and not torch.cuda.is_current_stream_capturing():
+        with _ws_lock:
+            w = _paged_words.get(dev.index)
+            if w is None:
+                w = torch.zeros(64, dtype=torch.int32, device=dev)
+                torch.cuda.current_stream(dev).synchronize()    # other streams may use it next
+                _paged_words[dev.index] = w
     return w
 
 
@@ -523,16 +530,38 @@ def reset_paged_status(device: Optional[torch.device] = None) -> None:
         reset_device_status(w)
 
 
-def _i32_vector(t: torch.Tensor, n: int, name: str, dev: torch.device) -> torch.Tensor:
-    _require(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and tuple(t.shape) == (n,) and t.device == dev,
-             f"{name} must be int32 [{n}] on {dev}")
-    return t.contiguous()
+# Single-token steps run in a few microseconds on the GPU, so these checks are
+# written to cost little where they pass: messages are only put together to be raised.
+def _bad(msg: str) -> None:
+    raise ValueError(msg)
 
 
-def _block_table(t: torch.Tensor, b: int, dev: torch.device) -> None:
-    _require(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.dim() == 2 and t.shape[0] == b and
-             t.shape[1] >= 1 and t.device == dev and t.is_contiguous(),
-             f"block_table must be contiguous int32 [{b}, max_blocks] on {dev}")
+def _i32_vector(t: torch.Tensor, n: int, name: str, index: int) -> torch.Tensor:
+    if t.dtype != torch.int32 or t.shape != (n,) or t.get_device() != index:
+        _bad(f"{name} must be int32 [{n}] on cuda:{index}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _block_table(t: torch.Tensor, index: int) -> Tuple[int, int]:
+    if t.dtype != torch.int32 or t.dim() != 2 or t.get_device() != index or not t.is_contiguous() or t.shape[1] < 1:
+        _bad(f"block_table must be contiguous int32 [b, max_blocks] on cuda:{index}")
+    return t.shape
+
+
+class _OnDevice:
+    """Makes a device current for a launch, if another one is."""
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.back != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back != self.index:
+            torch.cuda.set_device(self.back)
 
 
 def extend_block_table(block_table: torch.Tensor, cache_seqlens: torch.Tensor, new_lens: torch.Tensor,
@@ -550,26 +579,30 @@ def extend_block_table(block_table: torch.Tensor, cache_seqlens: torch.Tensor, n
     quantize_kv skips.  slot_mapping goes to quantize_kv; cu_new and the lengths go to
     quantize_kv_blocks and the attention calls.
     """
-    _require(isinstance(block_table, torch.Tensor) and block_table.is_cuda and block_table.dim() == 2,
-             "block_table must be int32 [b, max_blocks] on CUDA")
-    dev, b = block_table.device, block_table.shape[0]
-    _block_table(block_table, b, dev)
-    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", dev)
-    new_lens = _i32_vector(new_lens, b, "new_lens", dev)
-    num_free = _i32_vector(num_free, 1, "num_free", dev)
-    _require(free_blocks.dtype == torch.int32 and free_blocks.dim() == 1 and free_blocks.device == dev,
-             f"free_blocks must be int32 [capacity] on {dev}")
-    free_blocks = free_blocks.contiguous()
+    if not block_table.is_cuda:
+        _bad("block_table must be int32 [b, max_blocks] on CUDA")
+    index = block_table.get_device()
+    b, cols = _block_table(block_table, index)
+    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", index)
+    new_lens = _i32_vector(new_lens, b, "new_lens", index)
+    num_free = _i32_vector(num_free, 1, "num_free", index)
+    if free_blocks.dim() != 1:
+        _bad("free_blocks must be int32 [capacity]")
+    capacity = free_blocks.shape[0]
+    free_blocks = _i32_vector(free_blocks, capacity, "free_blocks", index)
     n = int(max_new_tokens)
-    _require(0 <= n < 1 << 31, "max_new_tokens must be in [0, 2^31)")
+    if not 0 <= n < 1 << 31:
+        _bad("max_new_tokens must be in [0, 2^31)")
+    dev = block_table.device
     slots = torch.empty(n, dtype=torch.int64, device=dev)
     cu_new = torch.empty(b + 1, dtype=torch.int32, device=dev)
     lens = torch.empty(b, dtype=torch.int32, device=dev)
     left = torch.empty(1, dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        rc = lib().smla_extend_block_table(_ptr(block_table), block_table.shape[1], _ptr(cache_seqlens),
-                                           _ptr(new_lens), b, _ptr(free_blocks), free_blocks.numel(), _ptr(num_free),
-                                           n, _ptr(slots), _ptr(cu_new), _ptr(lens), _ptr(left), _stream(dev))
+    with _OnDevice(index):
+        rc = lib().smla_extend_block_table(block_table.data_ptr(), cols, cache_seqlens.data_ptr(),
+                                           new_lens.data_ptr(), b, free_blocks.data_ptr(), capacity,
+                                           num_free.data_ptr(), n, slots.data_ptr(), cu_new.data_ptr(),
+                                           lens.data_ptr(), left.data_ptr(), _raw_stream(index))
     _check(rc, "smla_extend_block_table")
     return slots, cu_new, lens, left
 
@@ -578,29 +611,33 @@ _Q8_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
 
 
 def _q8_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor) -> _Q8Cache:
-    _require(isinstance(k_cache, torch.Tensor) and k_cache.is_cuda and k_cache.dim() == 4 and
-             k_cache.dtype in _Q8_FORMATS and k_cache.shape[2] == BLOCK_SIZE and k_cache.shape[3] in (64, 128),
-             "k_cache must be e4m3 or int8 [num_blocks, h_kv, 64, 64 or 128] on CUDA")
-    nb, h_kv, _, d = k_cache.shape
+    fmt = _Q8_FORMATS.get(k_cache.dtype)
+    shape, index = k_cache.shape, k_cache.get_device()
+    if fmt is None or len(shape) != 4 or index < 0 or shape[2] != BLOCK_SIZE or shape[3] not in (64, 128):
+        _bad("k_cache must be e4m3 or int8 [num_blocks, h_kv, 64, 64 or 128] on CUDA")
+    nb, h_kv, _, d = shape
+    block = h_kv * BLOCK_SIZE * d
+    strides = []
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _require(t.dtype == k_cache.dtype and t.shape == k_cache.shape and t.device == k_cache.device,
-                 f"{name} must match k_cache's type, shape and device")
-        _require((h_kv == 1 or t.stride(1) == BLOCK_SIZE * d) and t.stride(2) == d and t.stride(3) == 1,
-                 f"{name} must be dense within a block")
+        if t.dtype != k_cache.dtype or t.shape != shape or t.get_device() != index:
+            _bad(f"{name} must match k_cache's type, shape and device")
+        st = t.stride()
+        if (h_kv > 1 and st[1] != BLOCK_SIZE * d) or st[2] != d or st[3] != 1:
+            _bad(f"{name} must be dense within a block")
+        strides.append(st[0] if nb > 1 else block)      # a lone block's stride is free to say anything
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _require(t.dtype == torch.float32 and tuple(t.shape) == (nb, h_kv) and t.device == k_cache.device and
-                 (h_kv == 1 or t.stride(1) == 1), f"{name} must be float32 [num_blocks, h_kv] on {k_cache.device}")
-    block = h_kv * BLOCK_SIZE * d     # a lone block's stride is free to say anything
-    return _Q8Cache(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), nb,
-                    k_cache.stride(0) if nb > 1 else block, v_cache.stride(0) if nb > 1 else block,
-                    k_scale.stride(0) if nb > 1 else h_kv, v_scale.stride(0) if nb > 1 else h_kv, h_kv, d,
-                    _Q8_FORMATS[k_cache.dtype])
+        st = t.stride()
+        if t.dtype != torch.float32 or t.shape != (nb, h_kv) or t.get_device() != index or (h_kv > 1 and st[1] != 1):
+            _bad(f"{name} must be float32 [num_blocks, h_kv] on cuda:{index}")
+        strides.append(st[0] if nb > 1 else h_kv)
+    return _Q8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, *strides, h_kv,
+                    d, fmt)
 
 
 def _rows16(t: torch.Tensor) -> torch.Tensor:
     """t [n, h, d] with dense rows that 16-byte loads can read; a copy where it has none."""
-    ok = t.stride(2) == 1 and t.stride(0) % 8 == 0 and t.stride(1) % 8 == 0 and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
+    a, b, c = t.stride()
+    return t if c == 1 and a % 8 == 0 and b % 8 == 0 and t.data_ptr() % 16 == 0 else t.contiguous()
 
 
 def quantize_kv_blocks(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -622,23 +659,23 @@ def quantize_kv_blocks(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, 
     paged_status(), or check_device_status=True to synchronise and raise.
     """
     cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
+    index = k_cache.get_device()
+    shape = (k.shape[0], cache.h_kv, cache.head_dim)
     for name, t in (("k", k), ("v", v)):
-        _require(t.dtype == torch.bfloat16 and t.dim() == 3 and tuple(t.shape[1:]) == (cache.h_kv, cache.head_dim) and
-                 t.shape[0] == k.shape[0] and t.device == dev,
-                 f"{name} must be bf16 [total, {cache.h_kv}, {cache.head_dim}] on {dev}")
-    b = block_table.shape[0]
-    _block_table(block_table, b, dev)
-    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", dev)
-    new_seqlens = _i32_vector(new_seqlens, b, "new_seqlens", dev)
-    cu_new = _i32_vector(cu_new, b + 1, "cu_new", dev)
+        if t.dtype != torch.bfloat16 or t.shape != shape or t.get_device() != index:
+            _bad(f"{name} must be bf16 [total, {cache.h_kv}, {cache.head_dim}] on cuda:{index}")
+    b, cols = _block_table(block_table, index)
+    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", index)
+    new_seqlens = _i32_vector(new_seqlens, b, "new_seqlens", index)
+    cu_new = _i32_vector(cu_new, b + 1, "cu_new", index)
     k, v = _rows16(k), _rows16(v)
-    with torch.cuda.device(dev):
-        word = _paged_word(dev)
-        rc = lib().smla_quantize_kv_blocks(_ptr(k), _ptr(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                                           k.shape[0], ctypes.byref(cache), _ptr(block_table), block_table.shape[1],
-                                           b, _ptr(cache_seqlens), _ptr(new_seqlens), _ptr(cu_new), _ptr(word),
-                                           _stream(dev))
+    ks, vs = k.stride(), v.stride()
+    with _OnDevice(index):
+        word = _paged_word(k_cache.device)
+        rc = lib().smla_quantize_kv_blocks(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], shape[0],
+                                           ctypes.byref(cache), block_table.data_ptr(), cols, b,
+                                           cache_seqlens.data_ptr(), new_seqlens.data_ptr(), cu_new.data_ptr(),
+                                           _ptr(word), _raw_stream(index))
     _check(rc, "smla_quantize_kv_blocks")
     if check_device_status and word is not None:
         _raise_on_flags(word, "smla_quantize_kv_blocks")
@@ -687,67 +724,77 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     keeps its own) and flags go to paged_status().
     """
     cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    _require(isinstance(q, torch.Tensor) and q.dtype == torch.bfloat16 and q.device == dev and
-             q.dim() == (4 if cu_seqlens_q is None else 3) and q.shape[-1] == cache.head_dim,
-             f"q must be bf16 [b, s_q, h_q, {cache.head_dim}], or [total_q, h_q, {cache.head_dim}] with cu_seqlens_q, "
-             f"on {dev}")
-    b = block_table.shape[0]
-    _block_table(block_table, b, dev)
-    h_q = q.shape[-2]
-    _require(h_q >= 1 and h_q % cache.h_kv == 0, "h_q must be a multiple of h_kv")
+    index, d = k_cache.get_device(), cache.head_dim
     shape = q.shape
-    s_q = 0
+    if (q.dtype != torch.bfloat16 or q.get_device() != index or len(shape) != (4 if cu_seqlens_q is None else 3) or
+            shape[-1] != d):
+        _bad(f"q must be bf16 [b, s_q, h_q, {d}], or [total_q, h_q, {d}] with cu_seqlens_q, on cuda:{index}")
+    b, cols = _block_table(block_table, index)
+    h_q = shape[-2]
+    if h_q < 1 or h_q % cache.h_kv:
+        _bad("h_q must be a multiple of h_kv")
+    s_q, cu = 0, None
     if cu_seqlens_q is None:
-        _require(q.shape[0] == b, f"q must hold {b} requests")
-        s_q = q.shape[1]
+        if shape[0] != b:
+            _bad(f"q must hold {b} requests")
+        s_q = shape[1]
         if max_seqlen_q is None:
             max_seqlen_q = s_q
         q = q.flatten(0, 1)
     else:
-        cu_seqlens_q = _i32_vector(cu_seqlens_q, b + 1, "cu_seqlens_q", dev)
+        cu_seqlens_q = _i32_vector(cu_seqlens_q, b + 1, "cu_seqlens_q", index)
+        cu = cu_seqlens_q.data_ptr()
     q = _rows16(q)
     total = q.shape[0]
-    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", dev)
+    cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", index)
     if alibi_slopes is not None:
-        _require(alibi_slopes.dtype == torch.float32 and tuple(alibi_slopes.shape) == (h_q,) and
-                 alibi_slopes.device == dev, f"alibi_slopes must be float32 [{h_q}] on {dev}")
+        if alibi_slopes.dtype != torch.float32 or alibi_slopes.shape != (h_q,) or alibi_slopes.get_device() != index:
+            _bad(f"alibi_slopes must be float32 [{h_q}] on cuda:{index}")
         alibi_slopes = alibi_slopes.contiguous()
     if prefix_lens is not None:
-        _require(causal, "prefix_lens needs causal=True")
-        prefix_lens = _i32_vector(prefix_lens, b, "prefix_lens", dev)
+        if not causal:
+            _bad("prefix_lens needs causal=True")
+        prefix_lens = _i32_vector(prefix_lens, b, "prefix_lens", index)
     if doc_bounds is not None:
-        _require(doc_bounds.dtype == torch.int32 and tuple(doc_bounds.shape) == (total, 2) and
-                 doc_bounds.device == dev, f"doc_bounds must be int32 [{total}, 2] on {dev}")
+        if doc_bounds.dtype != torch.int32 or doc_bounds.shape != (total, 2) or doc_bounds.get_device() != index:
+            _bad(f"doc_bounds must be int32 [{total}, 2] on cuda:{index}")
         doc_bounds = doc_bounds.contiguous()
         if doc_bounds.data_ptr() % 8:
             doc_bounds = doc_bounds.clone()
     softcap = float(softcap)
-    _require(0.0 <= softcap < math.inf, "softcap must be >= 0 and finite")
-    scale = -1.0 if softmax_scale is None else float(softmax_scale)
-    _require(softmax_scale is None or 0.0 < scale < math.inf, "softmax_scale must be > 0 and finite")
+    if not 0.0 <= softcap < math.inf:
+        _bad("softcap must be >= 0 and finite")
+    scale = -1.0
+    if softmax_scale is not None:
+        scale = float(softmax_scale)
+        if not 0.0 < scale < math.inf:
+            _bad("softmax_scale must be > 0 and finite")
+    dev = k_cache.device
     if out is None:
         o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     else:
         o, lse = out
         for name, t, dt, sh in (("o", o, torch.bfloat16, shape), ("lse", lse, torch.float32, shape[:-1])):
-            _require(t.dtype == dt and t.shape == sh and t.device == dev and t.is_contiguous(),
-                     f"out: {name} must be contiguous {dt} {list(sh)} on {dev}")
-    with torch.cuda.device(dev):
-        nbytes = gqa_workspace_bytes(cache.head_dim, dev)
+            if t.dtype != dt or t.shape != sh or t.get_device() != index or not t.is_contiguous():
+                _bad(f"out: {name} must be contiguous {dt} {list(sh)} on {dev}")
+        o = o if o.data_ptr() % 16 == 0 else _bad("out: o must be 16-byte aligned")
+    with _OnDevice(index):
+        L = lib()
+        nbytes = L.smla_gqa_workspace_bytes(d, index)
         if workspace is None:
             word, scratch = _paged_word(dev), torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            at, room = scratch.data_ptr(), nbytes
         else:
-            _require(workspace.device == dev and workspace.is_contiguous() and workspace.dtype == torch.uint8 and
-                     workspace.numel() >= 256 + nbytes, f"workspace needs {256 + nbytes} bytes of uint8 on {dev}")
-            word, scratch = workspace[:256], workspace[256:]
-        rc = lib().smla_gqa_attention_with_kvcache(
-            _ptr(q), q.stride(0), q.stride(1), total, h_q, ctypes.byref(cache), _ptr(block_table),
-            block_table.shape[1], b, _ptr(cache_seqlens), _ptr(cu_seqlens_q), s_q,
-            total if max_seqlen_q is None else int(max_seqlen_q), 1 if causal else 0, scale, softcap,
-            _ptr(alibi_slopes), _ptr(prefix_lens), _ptr(doc_bounds), _ptr(o), _ptr(lse), _ptr(scratch),
-            scratch.numel(), _ptr(word), _stream(dev))
+            if (workspace.get_device() != index or not workspace.is_contiguous() or workspace.dtype != torch.uint8 or
+                    workspace.numel() < 256 + nbytes):
+                _bad(f"workspace needs {256 + nbytes} bytes of uint8 on {dev}")
+            word, at, room = workspace, workspace.data_ptr() + 256, workspace.numel() - 256
+        rc = L.smla_gqa_attention_with_kvcache(
+            q.data_ptr(), q.stride(0), q.stride(1), total, h_q, ctypes.byref(cache), block_table.data_ptr(), cols, b,
+            cache_seqlens.data_ptr(), cu, s_q, total if max_seqlen_q is None else int(max_seqlen_q),
+            1 if causal else 0, scale, softcap, _ptr(alibi_slopes), _ptr(prefix_lens), _ptr(doc_bounds),
+            o.data_ptr(), lse.data_ptr(), at, room, _ptr(word), _raw_stream(index))
     _check(rc, "smla_gqa_attention_with_kvcache")
     if check_device_status and word is not None:
         _raise_on_flags(word, "smla_gqa_attention_with_kvcache")

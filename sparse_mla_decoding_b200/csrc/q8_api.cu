@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -71,11 +72,24 @@ int tile_map(CUtensorMap* map, void* base, const smla_q8_cache* c, int64_t block
   return r == CUDA_SUCCESS ? SMLA_OK : smla::cuda_failure(cudaErrorInvalidValue);
 }
 
-int sm_count(int device, int* out) {
-  int sms = 0;
-  if (const cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device); e != cudaSuccess)
-    return smla::cuda_failure(e);
-  *out = sms > 0 ? sms : 1;
+constexpr int kMaxDevices = 64;
+
+// SM count of a device, and whether it is sm_100; asked of the runtime once.
+int device_facts(int device, int* sms, bool* sm100) {
+  static std::atomic<int> known[kMaxDevices];         // 0: not asked; else SMs * 2 + sm_100
+  if (device < 0 || device >= kMaxDevices) return SMLA_ERR_UNSUPPORTED;
+  int f = known[device].load(std::memory_order_relaxed);
+  if (f == 0) {
+    int n = 0, major = 0, minor = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device);
+    if (e != cudaSuccess) return smla::cuda_failure(e);
+    f = (n > 0 ? n : 1) * 2 + (major == 10 && minor == 0 ? 1 : 0);
+    known[device].store(f, std::memory_order_relaxed);
+  }
+  *sms = f >> 1;
+  *sm100 = f & 1;
   return SMLA_OK;
 }
 
@@ -144,7 +158,8 @@ int smla_quantize_kv_blocks(const void* k, const void* v, int64_t k_token_stride
 
 size_t smla_gqa_workspace_bytes(int head_dim, int device) {
   int sms = 0;
-  if ((head_dim != 64 && head_dim != 128) || sm_count(device, &sms)) return 0;
+  bool sm100 = false;
+  if ((head_dim != 64 && head_dim != 128) || device_facts(device, &sms, &sm100)) return 0;
   return workspace(head_dim, sms).total;
 }
 
@@ -167,12 +182,11 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(workspace_ptr, 256) || !aligned(doc_bounds, 8) ||
       !good_stride(q_token_stride) || !good_stride(q_head_stride))
     return SMLA_ERR_INVALID_ARGUMENT;
-  int dev = 0, sms = 0, major = 0, minor = 0;
+  int dev = 0, sms = 0;
+  bool sm100 = false;
   if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return smla::cuda_failure(e);
-  if (int rc = sm_count(dev, &sms)) return rc;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 0) return SMLA_ERR_UNSUPPORTED;
+  if (int rc = device_facts(dev, &sms, &sm100)) return rc;
+  if (!sm100) return SMLA_ERR_UNSUPPORTED;
   const Layout wl = workspace(cache->head_dim, sms);
   if (workspace_bytes < wl.total) return SMLA_ERR_INVALID_ARGUMENT;
 

@@ -135,10 +135,43 @@ __device__ __forceinline__ void row_pow2(float amax, float& up, float& down) {
   down = __uint_as_float((uint32_t)k << 23);
 }
 
+// Two fp32 operations in one instruction; each is rounded as the scalar one.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // tanh for score caps.  |x| <= 0.75: x P(x^2), P a degree-5 fit to tanh(x)/x in
 // relative error (1.6e-7 in fp32, fitted by reweighted least squares on
 // Chebyshev nodes), so a small score keeps its relative precision; larger |x|:
 // 1 - 2 / (1 + exp(2|x|)) with the sign of x.
+constexpr float kTanhSmall = 0.75f;
 __device__ __forceinline__ float tanh_small(float x) {
   const float z = x * x;
   float r = -0.004716585855931044f;
@@ -149,12 +182,41 @@ __device__ __forceinline__ float tanh_small(float x) {
   r = fmaf(r, z, 1.0f);
   return r * x;
 }
+__device__ __forceinline__ float2 tanh_small2(float2 x) {
+  const float2 z = mul2(x, x);
+  float2 r = fma2(both(-0.004716585855931044f), z, both(0.01958341710269451f));
+  r = fma2(r, z, both(-0.0533447191119194f));
+  r = fma2(r, z, both(0.13325412571430206f));
+  r = fma2(r, z, both(-0.33332958817481995f));
+  r = fma2(r, z, both(1.0f));
+  return mul2(r, x);
+}
 __device__ __forceinline__ float tanh_full(float x) {
   const float a = fabsf(x);
   float rc;
   asm("rcp.approx.f32 %0, %1;" : "=f"(rc) : "f"(1.f + ex2(a * (2.f * kLog2e))));
   const float big = copysignf(fmaf(-2.f, rc, 1.f), x);
-  return a <= 0.75f ? tanh_small(x) : big;
+  return a <= kTanhSmall ? tanh_small(x) : big;
+}
+
+// x_j = cap tanh(x_j fc) of n scores: where a warp has only small ones, by the
+// polynomial alone (one vote for the n scores).
+template <int N>
+__device__ __forceinline__ void cap_scores(float* x, float fc, float cap) {
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; j += 2) top = max3(top, fabsf(x[j]), fabsf(x[j + 1]));
+  if (__any_sync(0xffffffffu, !(top * fc <= kTanhSmall))) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = cap * tanh_full(x[j] * fc);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      const float2 y = mul2(tanh_small2(mul2(make_float2(x[j], x[j + 1]), both(fc))), both(cap));
+      x[j] = y.x;
+      x[j + 1] = y.y;
+    }
+  }
 }
 
 // log2 of a value scale relative to `base`, kept within 2^+-60 (a zero scale

@@ -463,11 +463,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       for (int i = 0; i < 2; ++i) {
         const float f = row_fac[i] * e.k_scale;
         if (p.cap > 0.f) {
-          const float fc = f * (p.scale / p.cap), cl = p.cap * kLog2e;
+          float x[16];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < 16; ++j) x[j] = S[j >> 1][2 * i + (j & 1)];
+          cap_scores<16>(x, f * (p.scale / p.cap), p.cap * kLog2e);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) S[j][2 * i + k] = cl * tanh_full(S[j][2 * i + k] * fc);
+          for (int j = 0; j < 16; ++j) S[j >> 1][2 * i + (j & 1)] = x[j];
         } else {
           const float fs = f * sl2;
 #pragma unroll

@@ -36,8 +36,12 @@ namespace {
 constexpr int kTileRows = 128;            // rows of a tile: the MMA's M
 constexpr int kTileKeys = 128;            // positions of a key tile
 constexpr int kThreads = 512;
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
-static_assert(256 * (kSoftmaxRegs + kOtherRegs) <= 65536, "the split must fit what the CTA was launched with");
+// Registers of the softmax warps and of the others: 256 threads of each share what
+// the CTA is launched with (512 x 128), which the launch checks.
+template <int D>
+constexpr int kSoftmaxRegs = D == 128 ? 184 : 192;
+template <int D>
+constexpr int kOtherRegs = 256 - kSoftmaxRegs<D>;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct KeyScales {                        // of the two cache blocks of a key tile
@@ -56,7 +60,7 @@ struct PrefillShared {                    // at a 1024-byte boundary
   uint32_t tmem;
   int lo, hi;                             // positions that any row sees
   float base_log2;
-  int q0;                                 // for the outputs
+  int q0, r, blocks;
   int64_t row0, rows_all;
 };
 
@@ -228,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     sm.lo = 0x7FFFFFFF;
     sm.hi = 0;
     sm.q0 = x.q0;
+    sm.r = r;
     sm.row0 = row0;
     sm.rows_all = rows_all;
     mbar_init_fence();
@@ -292,13 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
   const int last = sm.lo < end ? (end + kTileKeys - 1) / kTileKeys : first;
   if (tid == 0 && sm.hi > (int64_t)p.max_blocks * kBlk) report_status(p.status, kStatusBadBlockTable);
   const int tiles = max(last - first, 0);
+  if (tid == 256) sm.blocks = (end + kBlk - 1) / kBlk;
 
   if (warp < 8) {
     // ================================ softmax ================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
-    const uint32_t s_addr = tmem + 128 * w + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t o_addr = tmem + 256 + 128 * w + ((uint32_t)(32 * (warp & 3)) << 16);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<D>));
+    const uint32_t s_addr = tmem + 128 * w + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = s_addr + 256;
     const float slope = live && p.slopes ? p.slopes[hq] * kLog2e : 0.f;
     const float pos = (float)(x.len - x.n + t);
     const float fs = row_fac * p.scale * kLog2e;
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       for (int i = 0; i < tiles; ++i) {
         if (!(ok = bar_wait_warp(&sm.sfull[w], i & 1, p.status))) break;
         tc_fence_after();
-        const KeyScales ks = sm.scales[i & 3];
+        const volatile KeyScales& ks = sm.scales[i & 3];   // read where used: S needs the registers
         float S[128];
         tmem_ld32(s_addr, S);
         tmem_ld32(s_addr + 32, S + 32);
@@ -324,22 +328,23 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (p.cap > 0.f) {
-              const float c = fc * ks.k[h];
-#pragma unroll
-              for (int j = 0; j < 64; ++j) S[64 * h + j] = cl * tanh_full(S[64 * h + j] * c);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 64; ++j) S[64 * h + j] *= f[h];
+              cap_scores<32>(S + 64 * h, fc * ks.k[h], cl);
+              cap_scores<32>(S + 64 * h + 32, fc * ks.k[h], cl);
+              f[h] = 1.f;
             }
-            f[h] = 1.f;
-          }
-          if (p.slopes) {
-            const float d0 = pos - (float)j0;
+            if (p.slopes) {
+              float2 d = make_float2(pos - (float)(j0 + 64 * h), pos - (float)(j0 + 64 * h + 1));
 #pragma unroll
-            for (int j = 0; j < 128; ++j) S[j] = fmaf(-slope, fabsf(d0 - (float)j), S[j]);
+              for (int j = 0; j < 64; j += 2) {
+                const float2 x = mul2(make_float2(S[64 * h + j], S[64 * h + j + 1]), both(f[h]));
+                S[64 * h + j] = fmaf(-slope, fabsf(d.x - (float)j), x.x);
+                S[64 * h + j + 1] = fmaf(-slope, fabsf(d.y - (float)j), x.y);
+              }
+              f[h] = 1.f;
+            }
           }
         }
-        if (j0 < all_lo || j0 + kTileKeys > all_hi || ks.there != 3u) {
+        if (__any_sync(0xffffffffu, j0 < lo || j0 + kTileKeys > hi) || ks.there != 3u) {
           int a = lo - j0, b = hi - j0;
           if (!(ks.there & 1u)) a = max(a, kBlk);
           if (!(ks.there & 2u)) b = min(b, kBlk);
@@ -354,12 +359,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         float top[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float a[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 64; j += 4)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a[k] = fmaxf(a[k], S[64 * h + j + k]);
-          top[h] = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+          for (int j = 0; j < 64; j += 4) {
+            a[0] = max3(a[0], S[64 * h + j], S[64 * h + j + 1]);
+            a[1] = max3(a[1], S[64 * h + j + 2], S[64 * h + j + 3]);
+          }
+          top[h] = fmaxf(a[0], a[1]);
           top[h] = fmaf(top[h], f[h], ks.rel[h]);      // f > 0
         }
         const float peak = fmaxf(top[0], top[1]);
@@ -383,21 +389,23 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float sub = m == -INFINITY ? 0.f : ks.rel[h] - m;
-          float sum[2] = {0.f, 0.f};
+          float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t P[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const int at = 64 * h + 32 * c + 2 * j;
-              const float a = ex2(fmaf(S[at], f[h], sub)), b = ex2(fmaf(S[at + 1], f[h], sub));
-              sum[0] += a;
-              sum[1] += b;
-              P[j] = pack_f16(a, b);
+              float2 e = fma2(make_float2(S[at], S[at + 1]), both(f[h]), both(sub));
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum[j & 1] = add2(sum[j & 1], e);
+              P[j] = pack_f16(e.x, e.y);
             }
             tmem_st16(s_addr + 32 * h + 16 * c, P);
           }
-          l = fmaf(sum[0] + sum[1], ks.unrel[h], l);
+          sum[0] = add2(sum[0], sum[1]);
+          l = fmaf(sum[0].x + sum[0].y, ks.unrel[h], l);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -438,23 +446,23 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     }
   } else if (warp < 12) {
     // ================================ producers ================================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<D>));
     // Warp q of 4 converts rows 16q .. 16q + 15 of each cache block: lane = (row
     // % 8, 16-code chunk % 4); the two rows of a quarter warp land in the even
     // and odd chunks of the swizzle, so the stores have no bank conflicts.
     constexpr int kHalves = D / 64;                   // 64-byte halves of a row of codes
     constexpr int kLoads = 2 * 2 * kHalves;           // 16-byte loads of a thread and key tile
     const int q = warp - 8, sub = lane >> 2, c4 = lane & 3;
-    const int32_t* table = p.block_table + (int64_t)r * p.max_blocks;
-    const int reach0 = sm.lo / kBlk, reach1 = (end + kBlk - 1) / kBlk;   // blocks that some row sees
+    asm volatile("bar.sync 1, 128;" ::: "memory");    // sm.blocks
     // Table entries and scales of 32 blocks (16 key tiles), one a lane.
     int page = -1;
     float kscale = 0.f, vscale = 0.f;
     auto load_entries = [&](int b) {
       page = -1;
       kscale = vscale = 0.f;
-      if (b >= reach0 && b < reach1) {
-        page = table[b];
+      const volatile PrefillShared<D>& again = sm;    // seldom used, so not kept in registers
+      if (b >= again.lo / kBlk && b < again.blocks) { // a block that some row sees
+        page = p.block_table[(int64_t)again.r * p.max_blocks + b];
         if (page >= 0 && page < p.num_blocks) {
           kscale = __ldg(p.k_scale + page * p.k_scale_stride + head);
           vscale = __ldg(p.v_scale + page * p.v_scale_stride + head);
@@ -466,8 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     };
     load_entries(2 * first + lane);
     const float v0 = __shfl_sync(0xffffffffu, vscale, 0);
-    const float base = v0 > 0.f ? log2f(v0) : 0.f;
-    if (tid == 256) sm.base_log2 = base;
+    if (tid == 256) sm.base_log2 = v0 > 0.f ? log2f(v0) : 0.f;
     uint4 raw_codes[kLoads];                          // this thread's codes of one tile, keys or values
     const int code_off = (head * kBlk + 16 * q + sub) * D + 16 * c4;
     auto load_tile = [&](int i, const uint8_t* cache, int64_t stride, int pg0, int pg1) {
@@ -519,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       if (tid == 256) {
         KeyScales ks;
         ks.k[0] = k0, ks.k[1] = k1;
-        ks.rel[0] = rel_log2(w0, base), ks.rel[1] = rel_log2(w1, base);
+        const float from = sm.base_log2;
+        ks.rel[0] = rel_log2(w0, from), ks.rel[1] = rel_log2(w1, from);
         ks.unrel[0] = ex2(-ks.rel[0]), ks.unrel[1] = ex2(-ks.rel[1]);
         ks.there = (pg0 >= 0 ? 1u : 0u) | (pg1 >= 0 ? 2u : 0u);
         sm.scales[i & 3] = ks;
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       if (lane == 0) mbar_arrive1(&sm.vfull[st]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<D>));
     if (warp == 12 && tiles > 0) {
       // ================================ MMA ================================
       const uint32_t hi_d = smem_desc_hi_sw128(1024);
@@ -597,7 +605,7 @@ cudaError_t launch_as(const Q8Params& p, cudaStream_t stream) {
   cudaFuncAttributes at;
   if (const cudaError_t e = cudaFuncGetAttributes(&at, q8_prefill_kernel<D, kInt8, kMods>); e != cudaSuccess) return e;
   // a register split above what the CTA is launched with would wait for ever
-  if (at.numRegs * kThreads < 256 * (kSoftmaxRegs + kOtherRegs)) return cudaErrorInvalidConfiguration;
+  if (at.numRegs * kThreads < 256 * (kSoftmaxRegs<D> + kOtherRegs<D>)) return cudaErrorInvalidConfiguration;
   if (const cudaError_t e = cudaFuncSetAttribute(q8_prefill_kernel<D, kInt8, kMods>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
       e != cudaSuccess)
