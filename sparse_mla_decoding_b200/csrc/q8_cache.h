@@ -120,9 +120,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// 2^x, subnormal results flushed (a probability below 2^-126 of its row's
+// largest): without the flush the compiler scales around every one of them.
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -194,7 +196,7 @@ __device__ __forceinline__ float2 tanh_small2(float2 x) {
 __device__ __forceinline__ float tanh_full(float x) {
   const float a = fabsf(x);
   float rc;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(rc) : "f"(1.f + ex2(a * (2.f * kLog2e))));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + ex2(a * (2.f * kLog2e))));
   const float big = copysignf(fmaf(-2.f, rc, 1.f), x);
   return a <= kTanhSmall ? tanh_small(x) : big;
 }

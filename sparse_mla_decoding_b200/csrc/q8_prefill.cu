@@ -36,12 +36,11 @@ namespace {
 constexpr int kTileRows = 128;            // rows of a tile: the MMA's M
 constexpr int kTileKeys = 128;            // positions of a key tile
 constexpr int kThreads = 512;
-// Registers of the softmax warps and of the others: 256 threads of each share what
-// the CTA is launched with (512 x 128), which the launch checks.
-template <int D>
-constexpr int kSoftmaxRegs = D == 128 ? 184 : 192;
-template <int D>
-constexpr int kOtherRegs = 256 - kSoftmaxRegs<D>;
+// Registers of a thread after the split: the warps' shares are what the CTA was
+// launched with (512 x 128), which the launch checks.
+constexpr int kSoftmaxRegs = 192, kProducerRegs = 72, kMmaRegs = 56;
+constexpr int kSplitRegs = 256 * kSoftmaxRegs + 128 * kProducerRegs + 128 * kMmaRegs;
+static_assert(kSplitRegs <= 65536, "the split must fit what the CTA was launched with");
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct KeyScales {                        // of the two cache blocks of a key tile
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
 
   if (warp < 8) {
     // ================================ softmax ================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs<D>));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const uint32_t s_addr = tmem + 128 * w + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = s_addr + 256;
     const float slope = live && p.slopes ? p.slopes[hq] * kLog2e : 0.f;
     const float pos = (float)(x.len - x.n + t);
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float sub = m == -INFINITY ? 0.f : ks.rel[h] - m;
-          float2 sum[2] = {both(0.f), both(0.f)};
+          float2 sum = both(0.f);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t P[16];
@@ -399,13 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
               float2 e = fma2(make_float2(S[at], S[at + 1]), both(f[h]), both(sub));
               e.x = ex2(e.x);
               e.y = ex2(e.y);
-              sum[j & 1] = add2(sum[j & 1], e);
+              sum = add2(sum, e);
               P[j] = pack_f16(e.x, e.y);
             }
             tmem_st16(s_addr + 32 * h + 16 * c, P);
           }
-          sum[0] = add2(sum[0], sum[1]);
-          l = fmaf(sum[0].x + sum[0].y, ks.unrel[h], l);
+          l = fmaf(sum.x + sum.y, ks.unrel[h], l);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     }
   } else if (warp < 12) {
     // ================================ producers ================================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<D>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
     // Warp q of 4 converts rows 16q .. 16q + 15 of each cache block: lane = (row
     // % 8, 16-code chunk % 4); the two rows of a quarter warp land in the even
     // and odd chunks of the swizzle, so the stores have no bank conflicts.
@@ -550,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       if (lane == 0) mbar_arrive1(&sm.vfull[st]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs<D>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     if (warp == 12 && tiles > 0) {
       // ================================ MMA ================================
       const uint32_t hi_d = smem_desc_hi_sw128(1024);
@@ -605,7 +603,7 @@ cudaError_t launch_as(const Q8Params& p, cudaStream_t stream) {
   cudaFuncAttributes at;
   if (const cudaError_t e = cudaFuncGetAttributes(&at, q8_prefill_kernel<D, kInt8, kMods>); e != cudaSuccess) return e;
   // a register split above what the CTA is launched with would wait for ever
-  if (at.numRegs * kThreads < 256 * (kSoftmaxRegs<D> + kOtherRegs<D>)) return cudaErrorInvalidConfiguration;
+  if (at.numRegs * kThreads < kSplitRegs) return cudaErrorInvalidConfiguration;
   if (const cudaError_t e = cudaFuncSetAttribute(q8_prefill_kernel<D, kInt8, kMods>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
       e != cudaSuccess)
