@@ -10,7 +10,7 @@
 //             row of S from TMEM, writes P (f16) over it and, when its maximum
 //             grows by more than 2^8, rescales its row of O in TMEM.  Before
 //             that the eight warps bring Q in.
-//   8-11      producers: codes from global memory to registers (one block
+//   8-11      producers: codes from global memory to registers (two blocks
 //             ahead), to f16, to 128-byte-swizzled shared memory.
 //   12, 13    MMA of row tile 0 and 1: S_w = Q_w K^T (both operands in shared
 //             memory), then O_w += P_w V (P in TMEM).
@@ -52,9 +52,12 @@ constexpr int kScaleRing = 8;
 constexpr int kThreads = 512;
 // Registers of a thread after the split: the warps' shares are what the CTA was
 // launched with (512 x 128), which the launch checks.
-constexpr int kSoftmaxRegs = 160, kProducerRegs = 112, kMmaRegs = 80;
-constexpr int kSplitRegs = 256 * kSoftmaxRegs + 128 * kProducerRegs + 128 * kMmaRegs;
-static_assert(kSplitRegs <= 65536, "the split must fit what the CTA was launched with");
+template <int D>
+struct Split {
+  static constexpr int kSoftmax = D == 128 ? 168 : 176, kProducer = D == 128 ? 120 : 112, kMma = D == 128 ? 56 : 48;
+  static constexpr int kAll = 256 * kSoftmax + 128 * kProducer + 128 * kMma;
+  static_assert(kAll <= 65536, "the split must fit what the CTA was launched with");
+};
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct BlockScales {
@@ -69,7 +72,7 @@ struct PrefillShared {                    // at a 1024-byte boundary
   uint8_t v[kStages][kBlk * D * 2];
   BlockScales scales[kScaleRing];
   float row_fac[2 * kTileRows];
-  uint64_t kfull[kStages], vfull[kStages];
+  uint64_t full[kStages];                 // K and V of a block
   uint64_t sfull[2][2], pfull[2][2];      // [row tile][block % 2]
   uint64_t odone[2][2], qfull;
   uint32_t tmem;
@@ -241,8 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
   // ---- set-up
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      bar_init(&sm.kfull[s], 4);
-      bar_init(&sm.vfull[s], 4);
+      bar_init(&sm.full[s], 4);
     }
     for (int s = 0; s < 2; ++s) {
       for (int b = 0; b < 2; ++b) {
@@ -267,14 +269,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   const int w = warp >> 2;                            // row tile of a softmax warp
-  int lo = 0, hi = 0x7FFFFFFF, t = 0, hq = 0;
   if (warp < 8) {
     const int64_t row = row0 + tid;                   // of a softmax thread
     int a = 0x7FFFFFFF, b = 0;
     if (row < rows_all) {
-      t = (int)row / p.group, hq = head * p.group + (int)row % p.group;
-      q8_visible(p, x, t, lo, hi);
-      if (lo < hi) a = lo, b = hi;
+      q8_visible(p, x, (int)row / p.group, a, b);
+      if (a >= b) a = 0x7FFFFFFF, b = 0;
     }
     a = __reduce_min_sync(0xffffffffu, a);
     b = __reduce_max_sync(0xffffffffu, b);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
 
   if (warp < 8) {
     // ================================ softmax ================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split<D>::kSoftmax));
     // Q: each row scaled by a power of two, as f16.  Warp `warp` brings in the 32
     // rows of its own threads, a row of 16-byte chunks by neighbouring lanes.
     {
@@ -337,6 +337,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       if (lane == 0) mbar_arrive1(&sm.qfull);
     }
     const float row_fac = sm.row_fac[tid];            // written by this warp
+    int lo = 0, hi = 0x7FFFFFFF, t = 0, hq = 0;
+    if (row0 + tid < rows_all) {
+      t = (int)(row0 + tid) / p.group, hq = head * p.group + (int)(row0 + tid) % p.group;
+      q8_visible(p, x, t, lo, hi);
+    }
     const uint32_t s_addr = tmem + 128 * w + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = s_addr + 256;
     const float slope = p.slopes ? p.slopes[hq] * kLog2e : 0.f;
     const float pos = (float)(x.len - x.n + t);
@@ -346,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     bool ok = true;
     if (w == 0 || two) {
       for (int i = 0; i < blocks; ++i) {
-        // kfull (long complete) for the block's scales
-        if (!(ok = bar_wait_warp(&sm.kfull[i % kStages], (i / kStages) & 1, p.status))) break;
+        // the block's scales come through its (long complete) barrier
+        if (!(ok = bar_wait_warp(&sm.full[i % kStages], (i / kStages) & 1, p.status))) break;
         if (!(ok = bar_wait_warp(&sm.sfull[w][i & 1], (i >> 1) & 1, p.status))) break;
         tc_fence_after();
         const uint32_t sa = s_addr + 64 * (i & 1);
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     }
   } else if (warp < 12) {
     // ================================ producers ================================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<D>::kProducer));
     // Warp q of 4 converts rows 16q .. 16q + 15 of a block: lane = (row % 8,
     // 16-code chunk % 4); the two rows of a quarter warp land in the even and odd
     // chunks of the swizzle, so the stores have no bank conflicts.
@@ -529,51 +534,59 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         sts128(to + at1, f[0], f[1], f[2], f[3]);
       }
     };
-    uint4 kc[kLoads], vc[kLoads];                     // this thread's codes of the next block
-    int pg = __shfl_sync(0xffffffffu, page, 0);
-    if (blocks > 0) {
-      load_tile(kc, 0, p.k_cache, p.k_block_bytes, pg);
-      load_tile(vc, 0, p.v_cache, p.v_block_bytes, pg);
+    // This thread's codes of the next two blocks: a load takes longer than a block
+    // where many CTAs read the same lines.
+    uint4 kc[2][kLoads], vc[2][kLoads];
+    float ks[2], vs[2];                               // and their scales
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int pg = __shfl_sync(0xffffffffu, page, e);
+      ks[e] = __shfl_sync(0xffffffffu, kscale, e);
+      vs[e] = __shfl_sync(0xffffffffu, vscale, e);
+      if (e < blocks) {
+        load_tile(kc[e], e, p.k_cache, p.k_block_bytes, pg);
+        load_tile(vc[e], e, p.v_cache, p.v_block_bytes, pg);
+      }
     }
     bool ok = true;
-    for (int i = 0; i < blocks; ++i) {
-      const int st = i % kStages;
-      const float ks = __shfl_sync(0xffffffffu, kscale, i & 31), vs = __shfl_sync(0xffffffffu, vscale, i & 31);
-      const bool more = i + 1 < blocks;
-      if (more) {
-        if ((i & 31) == 31) load_entries(i + 1 + lane);
-        pg = __shfl_sync(0xffffffffu, page, (i + 1) & 31);
-      }
-      // both stages are free once S of block i - 2 is done, for it stands behind the
-      // product of block i - 4; every phase is waited for in turn, as a phase two
-      // behind cannot be told from the one asked for
-      if (i >= 2) {
-        ok = bar_wait_warp(&sm.sfull[0][i & 1], ((i - 2) >> 1) & 1, p.status);
-        if (ok && two) ok = bar_wait_warp(&sm.sfull[1][i & 1], ((i - 2) >> 1) & 1, p.status);
-        if (!ok) break;
-      }
-      // keys
-      store_tile(smem_u32(sm.k[st]), kc);
-      if (more) load_tile(kc, i + 1, p.k_cache, p.k_block_bytes, pg);
-      if (tid == 256) {
+    for (int i0 = 0; ok && i0 < blocks; i0 += 2) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = i0 + e;
+        if (i >= blocks) break;
+        const int st = i % kStages;
         BlockScales bs;
-        bs.k = ks;
-        bs.rel = rel_log2(vs, base);
+        bs.k = ks[e];
+        bs.rel = rel_log2(vs[e], base);
         bs.unrel = ex2(-bs.rel);
-        sm.scales[i % kScaleRing] = bs;
+        int pg = -1;
+        const bool more = i + 2 < blocks;
+        if (more) {
+          if (((i + 2) & 31) == 0) load_entries(i + 2 + lane);
+          pg = __shfl_sync(0xffffffffu, page, (i + 2) & 31);
+          ks[e] = __shfl_sync(0xffffffffu, kscale, (i + 2) & 31);
+          vs[e] = __shfl_sync(0xffffffffu, vscale, (i + 2) & 31);
+        }
+        // the stage is free once S of block i - 2 is done, for it stands behind the
+        // product of block i - 4; every phase is waited for in turn, as a phase two
+        // behind cannot be told from the one asked for
+        if (i >= 2) {
+          ok = bar_wait_warp(&sm.sfull[0][e], ((i - 2) >> 1) & 1, p.status);
+          if (ok && two) ok = bar_wait_warp(&sm.sfull[1][e], ((i - 2) >> 1) & 1, p.status);
+          if (!ok) break;
+        }
+        store_tile(smem_u32(sm.k[st]), kc[e]);
+        if (more) load_tile(kc[e], i + 2, p.k_cache, p.k_block_bytes, pg);
+        store_tile(smem_u32(sm.v[st]), vc[e]);
+        if (more) load_tile(vc[e], i + 2, p.v_cache, p.v_block_bytes, pg);
+        if (tid == 256) sm.scales[i % kScaleRing] = bs;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&sm.full[st]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&sm.kfull[st]);
-      // values
-      store_tile(smem_u32(sm.v[st]), vc);
-      if (more) load_tile(vc, i + 1, p.v_cache, p.v_block_bytes, pg);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&sm.vfull[st]);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<D>::kMma));
     const int ww = warp - 12;                         // row tile
     if (blocks > 0 && (ww == 0 || (ww == 1 && two))) {
       // ================================ MMA ================================
@@ -589,16 +602,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         mma_commit(&sm.sfull[ww][i & 1]);
       };
       for (int i = 0; ok && i < min(2, blocks); ++i) {
-        if (!(ok = bar_wait_warp(&sm.kfull[i], 0, p.status))) break;
+        if (!(ok = bar_wait_warp(&sm.full[i], 0, p.status))) break;
         tc_fence_after();
         s_tile(i);
       }
       for (int i = 0; ok && i < blocks; ++i) {
         const int st = i % kStages;
         const bool more = i + 2 < blocks;
-        // the producers store V of block i before K of block i + 1
-        ok = more ? bar_wait_warp(&sm.kfull[(i + 2) % kStages], ((i + 2) / kStages) & 1, p.status)
-                  : bar_wait_warp(&sm.vfull[st], (i / kStages) & 1, p.status);
+        if (more) ok = bar_wait_warp(&sm.full[(i + 2) % kStages], ((i + 2) / kStages) & 1, p.status);
         if (!ok || !(ok = bar_wait_warp(&sm.pfull[ww][i & 1], (i >> 1) & 1, p.status))) break;
         tc_fence_after();
         issue_pv(o_tmem, s_tmem + 64 * (i & 1), v_lo + (uint32_t)st * (kStage >> 4), hi_d, kIdPV, i > 0);
@@ -625,7 +636,7 @@ cudaError_t launch_as(const Q8Params& p, cudaStream_t stream) {
   cudaFuncAttributes at;
   if (const cudaError_t e = cudaFuncGetAttributes(&at, q8_prefill_kernel<D, kInt8, kMods>); e != cudaSuccess) return e;
   // a register split above what the CTA is launched with would wait for ever
-  if (at.numRegs * kThreads < kSplitRegs) return cudaErrorInvalidConfiguration;
+  if (at.numRegs * kThreads < Split<D>::kAll) return cudaErrorInvalidConfiguration;
   if (const cudaError_t e = cudaFuncSetAttribute(q8_prefill_kernel<D, kInt8, kMods>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
       e != cudaSuccess)
