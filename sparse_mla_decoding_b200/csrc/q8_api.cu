@@ -220,6 +220,8 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   p.causal = causal;
   p.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)cache->head_dim);
   p.cap = softcap;
+  p.cap_log2 = softcap * smla::kLog2e;
+  p.inv_cap_log2 = softcap > 0.f ? 1.0f / p.cap_log2 : 0.f;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.status = status;

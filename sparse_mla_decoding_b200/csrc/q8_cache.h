@@ -40,6 +40,7 @@ struct Q8Params {
   int causal;
   float scale;                    // softmax scale
   float cap;                      // 0: none
+  float cap_log2, inv_cap_log2;   // cap log2(e) and its inverse
   __nv_bfloat16* o;               // [total_q][h_q][d]
   float* lse;                     // [total_q][h_q]
   uint32_t* status;               // may be NULL

@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           float x[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[j] = S[j >> 1][2 * i + (j & 1)];
-          cap_scores<16>(x, f * (p.scale / p.cap), p.cap * kLog2e);
+          cap_scores<16>(x, f * sl2 * p.inv_cap_log2, p.cap_log2);
 #pragma unroll
           for (int j = 0; j < 16; ++j) S[j >> 1][2 * i + (j & 1)] = x[j];
         } else {

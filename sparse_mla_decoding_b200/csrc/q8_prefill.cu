@@ -52,9 +52,8 @@ constexpr int kScaleRing = 8;
 constexpr int kThreads = 512;
 // Registers of a thread after the split: the warps' shares are what the CTA was
 // launched with (512 x 128), which the launch checks.
-template <int D>
 struct Split {
-  static constexpr int kSoftmax = D == 128 ? 168 : 176, kProducer = D == 128 ? 120 : 112, kMma = D == 128 ? 56 : 48;
+  static constexpr int kSoftmax = 176, kProducer = 120, kMma = 40;
   static constexpr int kAll = 256 * kSoftmax + 128 * kProducer + 128 * kMma;
   static_assert(kAll <= 65536, "the split must fit what the CTA was launched with");
 };
@@ -71,15 +70,15 @@ struct PrefillShared {                    // at a 1024-byte boundary
   uint8_t k[kStages][kBlk * D * 2];
   uint8_t v[kStages][kBlk * D * 2];
   BlockScales scales[kScaleRing];
-  float row_fac[2 * kTileRows];
   uint64_t full[kStages];                 // K and V of a block
   uint64_t sfull[2][2], pfull[2][2];      // [row tile][block % 2]
   uint64_t odone[2][2], qfull;
   uint32_t tmem;
   int lo, hi;                             // positions that any row sees
   float base_log2;
-  int q0, r;
+  Q8Request x;
   int64_t row0, rows_all;
+  bool bad;                               // its offsets
 };
 
 __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
@@ -200,11 +199,20 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 // Byte offset of 16-byte chunk `chunk` (8 f16 values) of a row of Q: 64-wide
 // column blocks of 128 x 128 bytes, swizzled.
 __device__ __forceinline__ uint32_t operand_at(int row, int chunk) {
   return (uint32_t)((chunk >> 3) * (kTileRows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
+
+template <int D>
+constexpr int kRowLanes = D / 8;          // lanes that read or write a row of q or o
 
 // 2^x for x <= 127 on the FMA pipe (two at a time), for the share of the
 // exponentials that the special function units would be waited for: n = round(x)
@@ -238,22 +246,30 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
   // ---- which rows: request r may hold the items from cu[r] * group / 256 + r on
   // (one more than its rows fill); the last items, whose tokens see most, first
   const int64_t item = (int64_t)gridDim.x - 1 - blockIdx.x;
+  // The owner is the last request whose first item is at or before this one; the
+  // thread that tests a request has its lengths ready for the others.
   int r = -1;
   for (int i0 = 0; i0 < p.batch; i0 += kThreads) {
     const int i = i0 + tid;
-    bool before = false;
+    bool bad = false, before = false;
+    Q8Request mine{0, 0, 0, 0};
     if (i < p.batch) {
+      mine = q8_request(p, i, &bad);
       const int64_t c = p.cu_q ? max(p.cu_q[i], 0) : (int64_t)i * p.s_q;
       before = c * p.group / (2 * kTileRows) + i <= item;
     }
     const int c = __syncthreads_count(before);
+    if (tid == c - 1) {
+      sm.x = mine;
+      sm.bad = bad;
+    }
     r += c;
     if (c < kThreads) break;
   }
   if (r < 0) return;
-  bool bad;
-  const Q8Request x = q8_request(p, r, &bad);
-  if (bad) {
+  __syncthreads();
+  const Q8Request x = sm.x;
+  if (sm.bad) {
     if (tid == 0) report_status(p.status, kStatusBadSchedule);
     return;
   }
@@ -277,8 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     bar_init(&sm.qfull, 8);
     sm.lo = 0x7FFFFFFF;
     sm.hi = 0;
-    sm.q0 = x.q0;
-    sm.r = r;
     sm.row0 = row0;
     sm.rows_all = rows_all;
     mbar_init_fence();
@@ -314,60 +328,62 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
 
   if (warp < 8) {
     // ================================ softmax ================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split<D>::kSoftmax));
-    // Q: each row scaled by a power of two, as f16.  Warp `warp` brings in the 32
-    // rows of its own threads, a row of 16-byte chunks by neighbouring lanes.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split::kSoftmax));
+    // This thread's row: token, query head, and which positions it sees.
+    int lo = 0, hi = 0x7FFFFFFF, t = 0, hq = 0;
+    int64_t q_at = -1;                                // in q; -1: no row
+    if (row0 + tid < rows_all) {
+      t = (int)(row0 + tid) / p.group;
+      hq = head * p.group + (int)(row0 + tid) - t * p.group;
+      q8_visible(p, x, t, lo, hi);
+      q_at = (int64_t)(x.q0 + t) * p.q_token_stride + (int64_t)hq * p.q_head_stride;
+    }
+    // Q: each row scaled by a power of two, as f16.  A warp copies the 32 rows of its
+    // threads into their places as they are, a row by neighbouring lanes, then each
+    // thread converts its own row where it lies.
+    float row_fac;
     {
-      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRound = 8;
-      const int sub = lane / kLanes, chunk = lane % kLanes;
+      const int sub = lane / kRowLanes<D>, chunk = lane % kRowLanes<D>;
       const uint32_t qs = smem_u32(sm.q[w]);
+#pragma unroll 4
+      for (int k = 0; k < 32; k += 32 / kRowLanes<D>) {
+        const int64_t from = __shfl_sync(0xffffffffu, q_at, k + sub);
+        const uint32_t dst = qs + operand_at(32 * (warp & 3) + k + sub, chunk);
+        if (from >= 0)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p.q + from + 8 * chunk) : "memory");
+        else
+          sts128(dst, 0, 0, 0, 0);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
       auto lo_of = [](uint32_t v) { return __uint_as_float(v << 16); };
       auto hi_of = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
-      for (int i0 = 0; i0 < 32; i0 += kRound * kAtOnce) {
-        uint4 u[kRound];
+      const int rr = tid & 127;
+      float top = 0.f;
+      uint4 u[D / 8];
 #pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-          const int64_t row = row0 + 32 * warp + i0 + k * kAtOnce + sub;
-          u[k] = make_uint4(0, 0, 0, 0);
-          if (row < rows_all)
-            u[k] = __ldg(reinterpret_cast<const uint4*>(
-                             p.q + (int64_t)(x.q0 + (int)row / p.group) * p.q_token_stride +
-                             (int64_t)(head * p.group + (int)row % p.group) * p.q_head_stride) +
-                         chunk);
-        }
+      for (int k = 0; k < D / 8; ++k) u[k] = lds128(qs + operand_at(rr, k));
 #pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-          const int rr = 32 * (warp & 3) + i0 + k * kAtOnce + sub;
-          const uint32_t v[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-          float top = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = max3(top, fabsf(lo_of(v[j])), fabsf(hi_of(v[j])));
-#pragma unroll
-          for (int off = kLanes / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          float up, down;
-          row_pow2(top, up, down);
-          uint32_t f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = pack_f16(lo_of(v[j]) * up, hi_of(v[j]) * up);
-          sts128(qs + operand_at(rr, chunk), f[0], f[1], f[2], f[3]);
-          if (chunk == 0) sm.row_fac[kTileRows * w + rr] = down;
-        }
+      for (int k = 0; k < D / 8; ++k) {
+        const float a = max3(fabsf(lo_of(u[k].x)), fabsf(hi_of(u[k].x)), fabsf(lo_of(u[k].y)));
+        const float b = max3(fabsf(hi_of(u[k].y)), fabsf(lo_of(u[k].z)), fabsf(hi_of(u[k].z)));
+        top = max3(top, max3(a, b, fabsf(lo_of(u[k].w))), fabsf(hi_of(u[k].w)));
       }
+      float up;
+      row_pow2(top, up, row_fac);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k)
+        sts128(qs + operand_at(rr, k), pack_f16(lo_of(u[k].x) * up, hi_of(u[k].x) * up),
+               pack_f16(lo_of(u[k].y) * up, hi_of(u[k].y) * up), pack_f16(lo_of(u[k].z) * up, hi_of(u[k].z) * up),
+               pack_f16(lo_of(u[k].w) * up, hi_of(u[k].w) * up));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive1(&sm.qfull);
-    }
-    const float row_fac = sm.row_fac[tid];            // written by this warp
-    int lo = 0, hi = 0x7FFFFFFF, t = 0, hq = 0;
-    if (row0 + tid < rows_all) {
-      t = (int)(row0 + tid) / p.group, hq = head * p.group + (int)(row0 + tid) % p.group;
-      q8_visible(p, x, t, lo, hi);
     }
     const uint32_t s_addr = tmem + 128 * w + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = s_addr + 256;
     const float slope = p.slopes ? p.slopes[hq] * kLog2e : 0.f;
     const float pos = (float)(x.len - x.n + t);
     const float fs = row_fac * p.scale * kLog2e;
-    const float fc = p.cap > 0.f ? row_fac * p.scale / p.cap : 0.f, cl = p.cap * kLog2e;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     if (w == 0 || two) {
@@ -388,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         // capped and biased scores in place (f then is 1)
         if constexpr (kMods) {
           if (p.cap > 0.f) {
-            cap_scores<32>(S, fc * bs.k, cl);
-            cap_scores<32>(S + 32, fc * bs.k, cl);
+            cap_scores<32>(S, fs * bs.k * p.inv_cap_log2, p.cap_log2);
+            cap_scores<32>(S + 32, fs * bs.k * p.inv_cap_log2, p.cap_log2);
             f = 1.f;
           }
           if (p.slopes) {
@@ -467,17 +483,20 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         sum[0] = add2(sum[0], sum[1]);
         l = fmaf(sum[0].x + sum[0].y, bs.unrel, l);
       }
-      // ---- o = O / l, lse; what the loop did not need is taken from shared memory again
+      // ---- o = O / l, lse; o goes through Q's place (no product reads it any more),
+      // so that whole rows are stored by neighbouring lanes.  What the loop did not
+      // need is worked out anew: its registers are S's.
       if (ok && blocks > 0) ok = bar_wait_warp(&sm.odone[w][(blocks - 1) & 1], ((blocks - 1) >> 1) & 1, p.status);
       tc_fence_after();
       if (ok) {
-        const int64_t row = sm.row0 + tid;
-        const bool live = row < sm.rows_all;
-        const int64_t at = (int64_t)(sm.q0 + (int)row / p.group) * p.h_q + head * p.group + (int)row % p.group;
-        const bool none = m == -INFINITY;
+        int me;
+        asm volatile("mov.u32 %0, %%tid.x;" : "=r"(me));
+        const volatile PrefillShared<D>& v_sm = sm;
+        const int64_t row0 = v_sm.row0, rows_all = v_sm.rows_all;
+        const int q0 = v_sm.x.q0, head = blockIdx.y, lane = me & 31, warp = me >> 5;
+        const bool none = m == -INFINITY && !(l != l);
         const float inv = none ? 0.f : ex2(sm.base_log2) / l;
-        if (live) p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
-        __nv_bfloat16* dst = p.o + at * D;
+        const uint32_t qs = smem_u32(sm.q[warp >> 2]);
 #pragma unroll 2
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -492,15 +511,29 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
                                                        none ? 0.f : o[8 * k + 2 * j + 1] * inv);
               v[j] = *reinterpret_cast<uint32_t*>(&b);
             }
-            if (live) *reinterpret_cast<uint4*>(dst + c + 8 * k) = make_uint4(v[0], v[1], v[2], v[3]);
+            sts128(qs + operand_at(me & 127, c / 8 + k), v[0], v[1], v[2], v[3]);
           }
+        }
+        int at = -1;                                  // this thread's row of o and lse
+        if (row0 + me < rows_all) {
+          const int t = (int)(row0 + me) / p.group;
+          at = (q0 + t) * p.h_q + head * p.group + (int)(row0 + me) - t * p.group;
+          p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+        __syncwarp();
+        const int sub = lane / kRowLanes<D>, chunk = lane % kRowLanes<D>;
+#pragma unroll 4
+        for (int k = 0; k < 32; k += 32 / kRowLanes<D>) {
+          const int to = __shfl_sync(0xffffffffu, at, k + sub);
+          const uint4 v = lds128(qs + operand_at(32 * (warp & 3) + k + sub, chunk));
+          if (to >= 0) reinterpret_cast<uint4*>(p.o + (int64_t)to * D)[chunk] = v;
         }
       }
       tc_fence_before();
     }
   } else if (warp < 12) {
     // ================================ producers ================================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<D>::kProducer));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split::kProducer));
     // Warp q of 4 converts rows 16q .. 16q + 15 of a block: lane = (row % 8,
     // 16-code chunk % 4); the two rows of a quarter warp land in the even and odd
     // chunks of the swizzle, so the stores have no bank conflicts.
@@ -611,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<D>::kMma));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split::kMma));
     const int ww = warp - 12;                         // row tile
     if (blocks > 0 && (ww == 0 || (ww == 1 && two))) {
       // ================================ MMA ================================
@@ -661,7 +694,7 @@ cudaError_t launch_as(const Q8Params& p, cudaStream_t stream) {
   cudaFuncAttributes at;
   if (const cudaError_t e = cudaFuncGetAttributes(&at, q8_prefill_kernel<D, kInt8, kMods>); e != cudaSuccess) return e;
   // a register split above what the CTA is launched with would wait for ever
-  if (at.numRegs * kThreads < Split<D>::kAll) return cudaErrorInvalidConfiguration;
+  if (at.numRegs * kThreads < Split::kAll) return cudaErrorInvalidConfiguration;
   if (const cudaError_t e = cudaFuncSetAttribute(q8_prefill_kernel<D, kInt8, kMods>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
       e != cudaSuccess)
