@@ -102,8 +102,8 @@ struct Layout {
 Layout workspace(int head_dim, int ctas) {
   const size_t parts = (size_t)ctas * smla::kQ8DecodeWarps;
   Layout l;
-  l.lse_off = align256(2 * parts * 16 * (size_t)head_dim * sizeof(float));
-  l.meta_off = l.lse_off + align256(2 * parts * 16 * sizeof(float));
+  l.lse_off = align256(2 * parts * smla::kQ8PartRows * (size_t)head_dim * sizeof(float));
+  l.meta_off = l.lse_off + align256(2 * parts * smla::kQ8PartRows * sizeof(float));
   l.total = l.meta_off + align256(parts * 8 * sizeof(int32_t));
   return l;
 }
@@ -238,7 +238,7 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   scratch.o = reinterpret_cast<float*>(ws);
   scratch.lse = reinterpret_cast<float*>(ws + wl.lse_off);
   scratch.meta = reinterpret_cast<int32_t*>(ws + wl.meta_off);
-  const cudaError_t e = smla::launch_q8_decode(p, int8, k_map, v_map, scratch, sms,
+  const cudaError_t e = smla::launch_q8_decode(p, int8, max_seqlen_q * p.group, k_map, v_map, scratch, sms,
                                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SMLA_OK : smla::cuda_failure(e);
 }

@@ -11,22 +11,25 @@
 
 namespace smla {
 
-constexpr int kQ8DecodeWarps = 8;        // warps of a CTA, each with its own range of the work
+constexpr int kQ8DecodeWarps = 12;       // most warps of a CTA, each with its own range of the work
+constexpr int kQ8PartRows = 16;          // rows of a partial
 constexpr int64_t kQ8MinVisits = 2;      // least blocks of a warp's range
 
 // Rows (tokens times the head group) of a request up to which the decode kernel
 // runs: it reads the cache once per 16 rows.
 constexpr int64_t kQ8DecodeRows = 32;
 
-// Partials of the decode kernel: two slots of 16 rows for each warp.
+// Partials of the decode kernel: two slots of kQ8PartRows rows for each warp.
 struct Q8Scratch {
-  float* o;                              // [2 parts][16][d], normalised
-  float* lse;                            // [2 parts][16], log2
+  float* o;                              // [2 parts][kQ8PartRows][d], normalised
+  float* lse;                            // [2 parts][kQ8PartRows], log2
   int32_t* meta;                         // [parts][8]: the unit a part begins inside
 };
 
-cudaError_t launch_q8_decode(const Q8Params& p, bool int8, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                             const Q8Scratch& scratch, int ctas, cudaStream_t stream);
+// `rows`: the most rows (tokens times the head group) of a request, as far as the
+// caller knows; it picks the row tile.
+cudaError_t launch_q8_decode(const Q8Params& p, bool int8, int rows, const CUtensorMap& k_map,
+                             const CUtensorMap& v_map, const Q8Scratch& scratch, int ctas, cudaStream_t stream);
 
 // The tensor-core kernel for many new tokens: no scratch, one CTA per 256 rows.
 cudaError_t launch_q8_prefill(const Q8Params& p, bool int8, cudaStream_t stream);

@@ -7,20 +7,28 @@
 //   x_j -= slope_h |p - j| with slopes;
 //   lse = ln sum_j exp(x_j),  o = sum_j exp(x_j - lse) v_j.
 //
-// Work: one visit is one cache block of one (request, 16-row tile, KV head); the
-// rows of a tile are (token, head of the group) pairs, so a block's codes are
-// read once for the whole group.  All visits, in (request, row tile, head, block)
-// order, are cut into equal ranges, one per warp; a warp walks its range alone,
-// with its own ring of TMA tiles, and no warp waits for another.  A range that
-// holds a whole (request, tile, head) writes o itself; pieces of one go to the
-// workspace as normalised partials that q8_combine_kernel merges by their lse.
+// Work: one visit is one cache block of one (request, row tile, KV head); the rows
+// of a tile are (token, head of the group) pairs, so a block's codes are read once
+// for the whole group.  All visits, in (request, row tile, head, block) order, are
+// cut into equal ranges, one per warp; a warp walks its range alone, with its own
+// ring of TMA tiles, and no warp waits for another.  A range that holds a whole
+// (request, tile, head) writes o itself; pieces of one go to the workspace as
+// normalised partials that q8_combine_kernel merges by their lse.
 //
-// Numbers: codes are exact in f16 and q is scaled by a power of two per row, so
-// S = QK^T (m16n8k16, fp32 accumulators) has no input rounding and the scales
-// multiply in fp32.  A value scale rides in the exponent,
+// Products: S^T = K Q^T and O^T = V^T P^T on m16n8k16, so the cache's codes fill
+// the 16-row side and a tile has 8 rows (one MMA column block) or 16 (two): a group
+// of 8 heads wastes nothing, where rows on the 16-row side would double the
+// products and the softmax.  The codes go to f16 in registers, once for all rows.
+//
+// Numbers: codes are exact in f16 and q is scaled by a power of two per row, so S
+// has no input rounding and the scales multiply in fp32.  A value scale rides in
+// the exponent,
 //   p_j = 2^(x_j + log2 v_scale - m),
 // so one accumulator holds blocks of different scales; the sum of the softmax
-// takes the factor out again per block.  P is rounded to f16 once (2^-12).
+// takes the factor out again per block.  P is rounded to f16 once (2^-11).
+//
+// Bound by HBM: d + 1/16 bytes a key, value and head; what has to keep up is the
+// conversion, about 470 instructions a warp and block (16 KB at d = 128).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -34,14 +42,17 @@ namespace smla {
 
 namespace {
 
-constexpr int kRows = 16;                 // rows of a tile: the MMA's M
-constexpr int kWarps = kQ8DecodeWarps;
+constexpr int kPartRows = kQ8PartRows;    // rows of a partial slot
 constexpr int kRing = 64;                 // visits whose table entries a warp keeps
 constexpr int kSpanTokens = 16;           // document bounds are scanned up to this many new tokens
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-template <int D>
-constexpr int kTileSlots = D == 128 ? 3 : 6;   // 24 KB of tiles per warp
+// Warps of a CTA and tiles of a warp's ring: 192 KB of tiles in all.  8 rows take
+// under 170 registers, 16 rows up to 255.
+template <int NT>
+constexpr int kWarpsOf = NT == 1 ? 12 : 8;
+template <int D, int NT>
+constexpr int kTileSlots = 192 * 1024 / (kBlk * D * kWarpsOf<NT>);
 
 struct Entry {                            // one visit of the ring
   int block, head;                        // cache block (-1: nothing to read) and KV head
@@ -69,18 +80,23 @@ __device__ __forceinline__ void block_span(const Q8Params& p, const Q8Request& x
   count = max(1, end - first);
 }
 
-__device__ __forceinline__ int row_tiles(const Q8Params& p, int n) { return (n * p.group + kRows - 1) / kRows; }
+template <int NT>
+__device__ __forceinline__ int row_tiles(const Q8Params& p, int n) {
+  return (n * p.group + 8 * NT - 1) / (8 * NT);
+}
 
+template <int NT>
 __device__ __forceinline__ int64_t visits_of(const Q8Params& p, int r) {
   bool bad;
   const Q8Request x = q8_request(p, r, &bad);
   if (x.n == 0) return 0;
   int first, count;
   block_span(p, x, first, count);
-  return (int64_t)p.h_kv * row_tiles(p, x.n) * count;
+  return (int64_t)p.h_kv * row_tiles<NT>(p, x.n) * count;
 }
 
 // A position in the list of visits.
+template <int NT>
 struct Cursor {
   int r;
   Q8Request x;
@@ -90,7 +106,7 @@ struct Cursor {
     bool bad;
     x = q8_request(p, r, &bad);
     block_span(p, x, first, count);
-    units = p.h_kv * row_tiles(p, x.n);
+    units = p.h_kv * row_tiles<NT>(p, x.n);
   }
   // to visit `off` of the requests from r on
   __device__ __forceinline__ void seek(const Q8Params& p, int64_t off) {
@@ -139,17 +155,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D>
+// 8 x 8 f16 values, a row's pairs by its four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t t;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
+  return t;
+}
+
+template <int D, int NT>
 struct Shared {                           // at a 1024-byte boundary: the tiles' swizzle pattern
-  uint8_t tile[kWarps][kTileSlots<D>][kBlk * D];
-  Entry ring[kWarps][kRing];
-  uint64_t full[kWarps][kTileSlots<D>];
-  int64_t before[kWarps * 32 + 1];        // visits before each thread's requests
-  int64_t warp_sum[kWarps];
+  uint8_t tile[kWarpsOf<NT>][kTileSlots<D, NT>][kBlk * D];
+  Entry ring[kWarpsOf<NT>][kRing];
+  uint64_t full[kWarpsOf<NT>][kTileSlots<D, NT>];
+  int64_t before[kWarpsOf<NT> * 32 + 1];  // visits before each thread's requests
+  int64_t warp_sum[kWarpsOf<NT>];
 };
 
-template <int D>
-constexpr int kSharedBytes = sizeof(Shared<D>) + 1024;
+template <int D, int NT>
+constexpr int kSharedBytes = sizeof(Shared<D, NT>) + 1024;
 
 // Whole warp: the phase of `bar` has completed, within the time limit.
 __device__ __forceinline__ bool tile_ready(uint64_t* bar, uint32_t phase, uint32_t* status) {
@@ -159,22 +182,25 @@ __device__ __forceinline__ bool tile_ready(uint64_t* bar, uint32_t phase, uint32
 
 }  // namespace
 
-// One warp: thread (g, c) = (lane / 4, lane % 4) holds rows g and g + 8 of a tile.
-// K codes: thread c takes d in [32c, 32c + 32) of key 8j + g, so the MMA's k
-// indices stand for a permutation of d that q follows.  V codes: thread (g, c)
-// takes d in [16g, 16g + 16) of keys 16i + {2c, 2c+1, 2c+8, 2c+9}; column n of
-// output tile t stands for d = 16n + t.  Both read patterns are free of bank
-// conflicts in the 128-byte swizzle of the tiles.
-template <int D, bool kInt8>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+// One warp: thread (g, c) = (lane / 4, lane % 4).  K codes: thread c takes d in [32c,
+// 32c + 32) (16c at d = 64) of keys 16i + g and 16i + g + 8, so the MMA's k indices
+// stand for a permutation of d that q follows.  V codes: thread (g, c) takes d in
+// [16g, 16g + 16) (8g) of keys 16i + {2c, 2c+1, 2c+8, 2c+9}; rows g and g + 8 of output
+// tile t stand for d = 16g + 2t and + 1.  Both read patterns are free of bank conflicts
+// in the swizzle of the tiles (two-way for V at d = 64).  The thread holds scores and
+// outputs of rows 2c and 2c + 1 of each column block.
+template <int D, bool kInt8, int NT>
+__global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
     q8_decode_kernel(const __grid_constant__ Q8Params p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, Q8Scratch scratch) {
-  constexpr int kSlots = kTileSlots<D>;
+  constexpr int kWarps = kWarpsOf<NT>, kRows = 8 * NT;
+  constexpr int kSlots = kTileSlots<D, NT>;
   constexpr int kSteps = D / 16;          // k-steps of S
-  constexpr int kOut = D / 8;             // output tiles
-  constexpr int kPer = D / 4;             // q and o values of a thread and row
+  constexpr int kOut = D / 16;            // output tiles
+  constexpr int kPer = D / 4;             // q values of a thread and row
+  constexpr int kCols = D / 8;            // output values of a thread and row
   extern __shared__ uint8_t raw[];
-  Shared<D>& sm = *reinterpret_cast<Shared<D>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+  Shared<D, NT>& sm = *reinterpret_cast<Shared<D, NT>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   pdl_launch_dependents();
 
@@ -187,7 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int share = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
   int64_t mine = 0;
   for (int r = tid * share; r < min(p.batch, (tid + 1) * share); ++r) {
-    mine += visits_of(p, r);
+    mine += visits_of<NT>(p, r);
     if (blockIdx.x == 0) {
       bool bad;
       const Q8Request x = q8_request(p, r, &bad);
@@ -224,7 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (lane == 0) meta[0] = 0;
     return;
   }
-  Cursor cur;
+  Cursor<NT> cur;
   {
     int lo = 0, hi = kWarps * 32 - 1;               // the last share that starts at or before v0
     while (lo < hi) {
@@ -242,7 +268,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   // The loading side runs ahead of the computing one by the ring's tiles.  It
   // reads the table and the scales of up to 32 visits of a request at a time.
-  Cursor ahead = cur;
+  Cursor<NT> ahead = cur;
   int known = 0;                                    // visits whose entries are in the ring
   auto fill_ring = [&]() {
     const int64_t left = (int64_t)(ahead.units - ahead.unit) * ahead.count - ahead.blk;
@@ -287,10 +313,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   };
   for (int i = 0; i < kSlots; ++i) issue(i, i);
 
-  uint32_t Q[kSteps][4];
-  float O[kOut][4];
-  float row_fac[2], m[2], l[2], slope[2], pos[2];
-  int lo[2], hi[2], all_lo = 0, all_hi = 0;
+  uint32_t Q[NT][kSteps][2];
+  float O[NT][kOut][4];
+  // of rows 2c and 2c + 1 of each column block: power of two of q, softmax state, visibility
+  float row_fac[NT][2], m[NT][2], l[NT][2], slope[NT][2], pos[NT][2];
+  int lo[NT][2], hi[NT][2], all_lo = 0, all_hi = 0;
   float base_log2 = 0.f;
   bool opened = false;                              // base_log2 is set
   const float sl2 = p.scale * kLog2e;
@@ -301,58 +328,64 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     all_lo = 0;
     all_hi = 0x7FFFFFFF;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = rt * kRows + g + 8 * i, t = row / p.group, hq = head * p.group + row % p.group;
-      const bool live = t < cur.x.n;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      lo[i] = 0;
-      hi[i] = 0x7FFFFFFF;
-      slope[i] = 0.f;
-      pos[i] = (float)(cur.x.len - cur.x.n + t);
-      uint4 w[kPer / 8];
+    for (int nt = 0; nt < NT; ++nt) {
+      {                                             // q of row 8 nt + g
+        const int row = rt * kRows + 8 * nt + g, t = row / p.group, hq = head * p.group + row % p.group;
+        uint4 w[kPer / 8];
 #pragma unroll
-      for (int k = 0; k < kPer / 8; ++k) w[k] = make_uint4(0, 0, 0, 0);
-      if (live) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(cur.x.q0 + t) * p.q_token_stride +
-                                                          (int64_t)hq * p.q_head_stride + kPer * c);
+        for (int k = 0; k < kPer / 8; ++k) w[k] = make_uint4(0, 0, 0, 0);
+        if (t < cur.x.n) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(cur.x.q0 + t) * p.q_token_stride +
+                                                            (int64_t)hq * p.q_head_stride + kPer * c);
 #pragma unroll
-        for (int k = 0; k < kPer / 8; ++k) w[k] = __ldg(src + k);
-        q8_visible(p, cur.x, t, lo[i], hi[i]);
-        if (p.slopes) slope[i] = p.slopes[hq] * kLog2e;
-        all_lo = max(all_lo, lo[i]);
-        all_hi = min(all_hi, hi[i]);
-      }
-      float f[kPer], top = 0.f;
+          for (int k = 0; k < kPer / 8; ++k) w[k] = __ldg(src + k);
+        }
+        auto lo_of = [](uint32_t v) { return __uint_as_float(v << 16); };
+        auto hi_of = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
+        float top = 0.f;
 #pragma unroll
-      for (int k = 0; k < kPer / 8; ++k) {
-        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+        for (int k = 0; k < kPer / 8; ++k) {
+          const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[8 * k + 2 * j] = __uint_as_float(u[j] << 16);
-          f[8 * k + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-          top = fmaxf(top, fmaxf(fabsf(f[8 * k + 2 * j]), fabsf(f[8 * k + 2 * j + 1])));
+          for (int j = 0; j < 4; ++j) top = max3(top, fabsf(lo_of(u[j])), fabsf(hi_of(u[j])));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float up, down;
+        row_pow2(top, up, down);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) row_fac[nt][i] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + i));
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const uint4 a = w[s >> 1];
+          const uint32_t x = s & 1 ? a.z : a.x, y = s & 1 ? a.w : a.y;
+          Q[nt][s][0] = pack_f16(lo_of(x) * up, hi_of(x) * up);
+          Q[nt][s][1] = pack_f16(lo_of(y) * up, hi_of(y) * up);
         }
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      float up, down;
-      row_pow2(top, up, down);
-      row_fac[i] = down;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        Q[s][i] = pack_f16(f[4 * s] * up, f[4 * s + 1] * up);
-        Q[s][2 + i] = pack_f16(f[4 * s + 2] * up, f[4 * s + 3] * up);
+      for (int i = 0; i < 2; ++i) {
+        const int row = rt * kRows + 8 * nt + 2 * c + i, t = row / p.group, hq = head * p.group + row % p.group;
+        m[nt][i] = -INFINITY;
+        l[nt][i] = 0.f;
+        lo[nt][i] = 0;
+        hi[nt][i] = 0x7FFFFFFF;
+        slope[nt][i] = 0.f;
+        pos[nt][i] = (float)(cur.x.len - cur.x.n + t);
+        if (t < cur.x.n) {
+          q8_visible(p, cur.x, t, lo[nt][i], hi[nt][i]);
+          if (p.slopes) slope[nt][i] = p.slopes[hq] * kLog2e;
+          all_lo = max(all_lo, lo[nt][i]);
+          all_hi = min(all_hi, hi[nt][i]);
+        }
       }
-    }
-    for (int off = 16; off >= 1; off >>= 1) {
-      all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, off));
-      all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, off));
-    }
 #pragma unroll
-    for (int t = 0; t < kOut; ++t)
+      for (int t = 0; t < kOut; ++t)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) O[t][k] = 0.f;
+        for (int k = 0; k < 4; ++k) O[nt][t][k] = 0.f;
+    }
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
   };
 
   // The unit's result, or this warp's piece of it.
@@ -360,44 +393,43 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int head = cur.unit % p.h_kv, rt = cur.unit / p.h_kv;
     const float back = ex2(base_log2);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float s = l[i];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      const float inv = s == 0.f ? 0.f : back / s;
-      const float lse2 = s == 0.f ? -INFINITY : m[i] + log2f(s);
-      const int row = rt * kRows + g + 8 * i, t = row / p.group, hq = head * p.group + row % p.group;
-      if (t >= cur.x.n) continue;
-      if (whole) {
-        const int64_t at = (int64_t)(cur.x.q0 + t) * p.h_q + hq;
-        uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + kPer * c);
-        // columns 2c and 2c + 1 of output tile u stand for d = kOut (2c) + u and kOut (2c + 1) + u
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < 2; ++i) {
+        float s = l[nt][i];
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+        s += __shfl_xor_sync(0xffffffffu, s, 16);
+        const float inv = s == 0.f ? 0.f : back / s;
+        const float lse2 = s == 0.f ? -INFINITY : m[nt][i] + log2f(s);
+        const int in_tile = 8 * nt + 2 * c + i, row = rt * kRows + in_tile, t = row / p.group;
+        const int hq = head * p.group + row % p.group;
+        if (t >= cur.x.n) continue;
+        // rows g and g + 8 of output tile k: d = kCols g + 2k and + 1
+        if (whole) {
+          const int64_t at = (int64_t)(cur.x.q0 + t) * p.h_q + hq;
+          uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + kCols * g);
 #pragma unroll
-          for (int k = 0; k < kOut / 8; ++k) {
+          for (int k = 0; k < kOut / 4; ++k) {
             uint32_t u[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              __nv_bfloat162 b = __floats2bfloat162_rn(O[8 * k + 2 * j][2 * i + h] * inv,
-                                                       O[8 * k + 2 * j + 1][2 * i + h] * inv);
+              __nv_bfloat162 b = __floats2bfloat162_rn(O[nt][4 * k + j][i] * inv, O[nt][4 * k + j][2 + i] * inv);
               u[j] = *reinterpret_cast<uint32_t*>(&b);
             }
-            dst[h * (kOut / 8) + k] = make_uint4(u[0], u[1], u[2], u[3]);
+            dst[k] = make_uint4(u[0], u[1], u[2], u[3]);
           }
-        if (c == 0) p.lse[at] = lse2 * kLn2;
-      } else {
-        const int64_t slot = 2 * (int64_t)part + (begun_here ? 1 : 0);
-        float4* dst = reinterpret_cast<float4*>(scratch.o + (slot * kRows + g + 8 * i) * D + kPer * c);
+          if (g == 0) p.lse[at] = lse2 * kLn2;
+        } else {
+          const int64_t slot = 2 * (int64_t)part + (begun_here ? 1 : 0);
+          float4* dst = reinterpret_cast<float4*>(scratch.o + (slot * kPartRows + in_tile) * D + kCols * g);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int k = 0; k < kOut / 4; ++k)
-            dst[h * (kOut / 4) + k] = make_float4(O[4 * k][2 * i + h] * inv, O[4 * k + 1][2 * i + h] * inv,
-                                                  O[4 * k + 2][2 * i + h] * inv, O[4 * k + 3][2 * i + h] * inv);
-        if (c == 0) scratch.lse[slot * kRows + g + 8 * i] = lse2;
+          for (int k = 0; k < kOut / 2; ++k)
+            dst[k] = make_float4(O[nt][2 * k][i] * inv, O[nt][2 * k][2 + i] * inv, O[nt][2 * k + 1][i] * inv,
+                                 O[nt][2 * k + 1][2 + i] * inv);
+          if (g == 0) scratch.lse[slot * kPartRows + in_tile] = lse2;
+        }
       }
-    }
   };
 
   // Which parts share the unit this range begins inside, for the merge.
@@ -422,28 +454,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   for (; v < visits; ++v) {
     const Entry e = ring[v % kRing];
     const int j0 = (cur.first + cur.blk) * kBlk;
-    // ---- S = Q K^T
+    // ---- S^T = K Q^T
     if (!tile_ready(&full[slot], phase, p.status)) break;
-    float S[8][4];
-    const uint32_t kt = tiles + slot * (kBlk * D);
+    float S[NT][4][4];                              // [16 keys][key g: rows 2c, 2c + 1; key g + 8: the same]
     if (e.block >= 0) {
+      const uint32_t kt = tiles + slot * (kBlk * D) + g * D;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t row = kt + (8 * j + g) * D;
-        uint32_t w[D / 16];
-        if constexpr (D == 128) {
-          const uint4 a = lds128(row + (((2 * c) ^ g) << 4)), b = lds128(row + (((2 * c + 1) ^ g) << 4));
-          w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        } else {
-          const uint4 a = lds128(row + ((c ^ ((g >> 1) & 3)) << 4));
-          w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[2][D / 16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t row = kt + (16 * i + 8 * h) * D;
+          const uint4 a = lds128(row + (D == 128 ? ((2 * c) ^ g) << 4 : (c ^ ((g >> 1) & 3)) << 4));
+          w[h][0] = a.x, w[h][1] = a.y, w[h][2] = a.z, w[h][3] = a.w;
+          if constexpr (D == 128) {
+            const uint4 b = lds128(row + (((2 * c + 1) ^ g) << 4));
+            w[h][4] = b.x, w[h][5] = b.y, w[h][6] = b.z, w[h][7] = b.w;
+          }
         }
-        S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[nt][i][0] = S[nt][i][1] = S[nt][i][2] = S[nt][i][3] = 0.f;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          uint32_t b0, b1;
-          Q8Codes<kInt8>::to_f16(w[s], b0, b1);
-          mma16816(S[j], Q[s][0], Q[s][1], Q[s][2], Q[s][3], b0, b1);
+          uint32_t a0, a1, a2, a3;
+          Q8Codes<kInt8>::to_f16(w[0][s], a0, a2);
+          Q8Codes<kInt8>::to_f16(w[1][s], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(S[nt][i], a0, a1, a2, a3, Q[nt][s][0], Q[nt][s][1]);
         }
       }
     }
@@ -451,7 +488,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     issue(2 * v + kSlots, slot);
     if (++slot == kSlots) slot = 0, phase ^= 1;
     // ---- softmax
-    uint32_t P[4][4];
+    uint32_t P[NT][4][2];                           // [16 keys][keys 2c, 2c + 1 and + 8 of row g]
     if (e.block >= 0) {
       if (!opened) {
         base_log2 = e.v_scale > 0.f ? log2f(e.v_scale) : 0.f;
@@ -460,76 +497,82 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       const float rel = rel_log2(e.v_scale, base_log2), unrel = ex2(-rel);
       const bool edge = j0 < all_lo || j0 + kBlk > all_hi;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float f = row_fac[i] * e.k_scale;
-        if (p.cap > 0.f) {
-          float x[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = S[j >> 1][2 * i + (j & 1)];
-          cap_scores<16>(x, f * sl2 * p.inv_cap_log2, p.cap_log2);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) S[j >> 1][2 * i + (j & 1)] = x[j];
-        } else {
-          const float fs = f * sl2;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) S[j][2 * i + k] *= fs;
-        }
-        if (p.slopes) {
-          const float d0 = pos[i] - (float)(j0 + 2 * c);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) S[j][2 * i + k] -= slope[i] * fabsf(d0 - (float)(8 * j + k));
-        }
-        if (edge) {
-          const int a = lo[i] - j0 - 2 * c, b = hi[i] - j0 - 2 * c;
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (8 * j + k < a || 8 * j + k >= b) S[j][2 * i + k] = -INFINITY;
-        }
-      }
-      float top[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top[i] = fmaxf(top[i], fmaxf(S[j][2 * i], S[j][2 * i + 1]));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2)) + rel;
-      }
-      // P may grow to 2^8 before the accumulators are rescaled (f16 reaches 2^15)
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float now = fmaxf(m[i], top[i]);
-          const float a = now == -INFINITY ? 1.f : ex2(m[i] - now);
-          m[i] = now;
-          l[i] *= a;
+          const float f = row_fac[nt][i] * e.k_scale * sl2;
+          if (p.cap > 0.f) {
+            float x[8];
 #pragma unroll
-          for (int t = 0; t < kOut; ++t) {
-            O[t][2 * i] *= a;
-            O[t][2 * i + 1] *= a;
+            for (int j = 0; j < 8; ++j) x[j] = S[nt][j >> 1][2 * (j & 1) + i];
+            cap_scores<8>(x, f * p.inv_cap_log2, p.cap_log2);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) S[nt][j >> 1][2 * (j & 1) + i] = x[j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) S[nt][j >> 1][2 * (j & 1) + i] *= f;
+          }
+          if (p.slopes) {
+            const float d0 = pos[nt][i] - (float)(j0 + g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) S[nt][j >> 1][2 * (j & 1) + i] -= slope[nt][i] * fabsf(d0 - (float)(8 * j));
+          }
+          if (edge) {
+            const int a = lo[nt][i] - j0 - g, b = hi[nt][i] - j0 - g;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (8 * j < a || 8 * j >= b) S[nt][j >> 1][2 * (j & 1) + i] = -INFINITY;
           }
         }
       }
+      float top[NT][2];
+      bool grew = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float sub = m[i] == -INFINITY ? 0.f : rel - m[i];
-        float sum = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float a = fmaxf(S[nt][0][i], S[nt][0][2 + i]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j) a = max3(a, S[nt][j][i], S[nt][j][2 + i]);
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
+          top[nt][i] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16)) + rel;
+          grew |= top[nt][i] > m[nt][i] + 8.f;
+        }
+      // P may grow to 2^8 before the accumulators are rescaled (f16 reaches 2^15)
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float now = fmaxf(m[nt][i], top[nt][i]);
+            const float a = now == -INFINITY ? 1.f : ex2(m[nt][i] - now);
+            m[nt][i] = now;
+            l[nt][i] *= a;
+#pragma unroll
+            for (int t = 0; t < kOut; ++t) {
+              O[nt][t][i] *= a;
+              O[nt][t][2 + i] *= a;
+            }
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float sub[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sub[i] = m[nt][i] == -INFINITY ? 0.f : rel - m[nt][i];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float a = ex2(S[j][2 * i] + sub), b = ex2(S[j][2 * i + 1] + sub);
-          sum += a + b;
-          P[j >> 1][i + 2 * (j & 1)] = pack_f16(a, b);
+          const float a = ex2(S[nt][j >> 1][2 * (j & 1)] + sub[0]), b = ex2(S[nt][j >> 1][2 * (j & 1) + 1] + sub[1]);
+          sum[0] += a;
+          sum[1] += b;
+          P[nt][j >> 1][j & 1] = transpose8(pack_f16(a, b));
         }
-        l[i] = fmaf(sum, unrel, l[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) l[nt][i] = fmaf(sum[i], unrel, l[nt][i]);
       }
     }
-    // ---- O += P V
+    // ---- O^T += V^T P^T
     if (!tile_ready(&full[slot], phase, p.status)) break;
     const uint32_t vt = tiles + slot * (kBlk * D);
     if (e.block >= 0) {
@@ -555,15 +598,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           }
         }
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {          // output tiles 4q .. 4q + 3
-          uint32_t b0[4], b1[4];
-          Q8Codes<kInt8>::to_f16(__byte_perm(w[0][q], w[1][q], 0x5140), b0[0], b0[1]);
-          Q8Codes<kInt8>::to_f16(__byte_perm(w[0][q], w[1][q], 0x7362), b0[2], b0[3]);
-          Q8Codes<kInt8>::to_f16(__byte_perm(w[2][q], w[3][q], 0x5140), b1[0], b1[1]);
-          Q8Codes<kInt8>::to_f16(__byte_perm(w[2][q], w[3][q], 0x7362), b1[2], b1[3]);
+        for (int q = 0; q < D / 32; ++q)            // output tiles 2q and 2q + 1
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mma16816(O[4 * q + u], P[kk][0], P[kk][1], P[kk][2], P[kk][3], b0[u], b1[u]);
-        }
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a0, a1, a2, a3;
+            Q8Codes<kInt8>::to_f16(__byte_perm(w[0][q], w[1][q], h ? 0x7362 : 0x5140), a0, a1);
+            Q8Codes<kInt8>::to_f16(__byte_perm(w[2][q], w[3][q], h ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(O[nt][2 * q + h], a0, a1, a2, a3, P[nt][kk][0], P[nt][kk][1]);
+          }
       }
     }
     __syncwarp();
@@ -589,7 +632,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
 // Merges the pieces of a unit.  Part p whose range begins inside a unit that
 // parts first .. last share merges the rows p - first - 1 + k (last - first).
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__ Q8Params p, Q8Scratch scratch) {
   __shared__ float acc[4][D];
   __shared__ float wsum[4];
@@ -598,12 +641,13 @@ __global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__
   const int* meta = scratch.meta + (size_t)part * 8;
   if (meta[0] == 0) return;
   const int first = meta[1], last = meta[2], n = meta[4], rt = meta[6];
+  constexpr int kRows = 8 * NT;
   const int rows = min(kRows, n * p.group - rt * kRows);
   constexpr int kV = D / 32;
   for (int row = part - first - 1; row < rows; row += last - first) {
     auto slot_of = [&](int q) { return (int64_t)2 * q + (q == first ? 1 : 0); };
     float top = -INFINITY;
-    for (int q = first + lane; q <= last; q += 32) top = fmaxf(top, scratch.lse[slot_of(q) * kRows + row]);
+    for (int q = first + lane; q <= last; q += 32) top = fmaxf(top, scratch.lse[slot_of(q) * kPartRows + row]);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     float sum = 0.f, o[kV];
@@ -611,7 +655,7 @@ __global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__
     for (int k = 0; k < kV; ++k) o[k] = 0.f;
 #pragma unroll 4
     for (int q = first + warp; q <= last; q += 4) {
-      const int64_t at = slot_of(q) * kRows + row;
+      const int64_t at = slot_of(q) * kPartRows + row;
       const float lse = scratch.lse[at];
       const float w = lse == -INFINITY ? 0.f : ex2(lse - top);
       const float* src = scratch.o + at * D + kV * lane;
@@ -636,15 +680,16 @@ __global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__
 
 namespace {
 
-template <int D, bool kInt8>
+template <int D, bool kInt8, int NT>
 cudaError_t launch(const Q8Params& p, const CUtensorMap& k_map, const CUtensorMap& v_map, const Q8Scratch& scratch,
                    int ctas, cudaStream_t stream) {
+  constexpr int kWarps = kWarpsOf<NT>, kBytes = kSharedBytes<D, NT>;
   // per call: the attribute belongs to the current context and costs no launch
-  if (const cudaError_t e = cudaFuncSetAttribute(q8_decode_kernel<D, kInt8>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes<D>);
+  if (const cudaError_t e = cudaFuncSetAttribute(q8_decode_kernel<D, kInt8, NT>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
       e != cudaSuccess)
     return e;
-  q8_decode_kernel<D, kInt8><<<ctas, kWarps * 32, kSharedBytes<D>, stream>>>(p, k_map, v_map, scratch);
+  q8_decode_kernel<D, kInt8, NT><<<ctas, kWarps * 32, kBytes, stream>>>(p, k_map, v_map, scratch);
   if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -655,18 +700,25 @@ cudaError_t launch(const Q8Params& p, const CUtensorMap& k_map, const CUtensorMa
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q8_combine_kernel<D>, p, scratch);
+  return cudaLaunchKernelEx(&cfg, q8_combine_kernel<D, NT>, p, scratch);
+}
+
+template <int D, bool kInt8>
+cudaError_t launch_rows(const Q8Params& p, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                        const Q8Scratch& scratch, int ctas, cudaStream_t stream) {
+  return rows <= 8 ? launch<D, kInt8, 1>(p, k_map, v_map, scratch, ctas, stream)
+                   : launch<D, kInt8, 2>(p, k_map, v_map, scratch, ctas, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_q8_decode(const Q8Params& p, bool int8, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                             const Q8Scratch& scratch, int ctas, cudaStream_t stream) {
+cudaError_t launch_q8_decode(const Q8Params& p, bool int8, int rows, const CUtensorMap& k_map,
+                             const CUtensorMap& v_map, const Q8Scratch& scratch, int ctas, cudaStream_t stream) {
   if (p.d == 128)
-    return int8 ? launch<128, true>(p, k_map, v_map, scratch, ctas, stream)
-                : launch<128, false>(p, k_map, v_map, scratch, ctas, stream);
-  return int8 ? launch<64, true>(p, k_map, v_map, scratch, ctas, stream)
-              : launch<64, false>(p, k_map, v_map, scratch, ctas, stream);
+    return int8 ? launch_rows<128, true>(p, rows, k_map, v_map, scratch, ctas, stream)
+                : launch_rows<128, false>(p, rows, k_map, v_map, scratch, ctas, stream);
+  return int8 ? launch_rows<64, true>(p, rows, k_map, v_map, scratch, ctas, stream)
+              : launch_rows<64, false>(p, rows, k_map, v_map, scratch, ctas, stream);
 }
 
 }  // namespace smla
