@@ -96,15 +96,17 @@ int device_facts(int device, int* sms, bool* sm100) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Layout {
-  size_t lse_off, meta_off, total;
+  size_t cta_o_off, lse_off, cta_lse_off, meta_off, total;
 };
 
 Layout workspace(int head_dim, int ctas) {
-  const size_t parts = (size_t)ctas * smla::kQ8DecodeWarps;
+  const size_t warps = (size_t)ctas * smla::kQ8DecodeWarps, rows = 2 * smla::kQ8PartRows;
   Layout l;
-  l.lse_off = align256(2 * parts * smla::kQ8PartRows * (size_t)head_dim * sizeof(float));
-  l.meta_off = l.lse_off + align256(2 * parts * smla::kQ8PartRows * sizeof(float));
-  l.total = l.meta_off + align256(parts * 8 * sizeof(int32_t));
+  l.cta_o_off = align256(rows * warps * (size_t)head_dim * sizeof(float));
+  l.lse_off = l.cta_o_off + align256(rows * (size_t)ctas * (size_t)head_dim * sizeof(float));
+  l.cta_lse_off = l.lse_off + align256(rows * warps * sizeof(float));
+  l.meta_off = l.cta_lse_off + align256(rows * (size_t)ctas * sizeof(float));
+  l.total = l.meta_off + align256((size_t)ctas * 8 * sizeof(int32_t));
   return l;
 }
 
@@ -171,8 +173,10 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
                                     void* o, float* lse, void* workspace_ptr, size_t workspace_bytes,
                                     uint32_t* status, void* stream) {
   if (int rc = check_cache(cache)) return rc;
-  if (h_q < 1 || h_q % cache->h_kv != 0 || batch < 0 || batch > (1 << 28) || max_blocks < 1 || total_q < 0 ||
-      total_q > 0x7FFFFFFF || total_q * h_q > 0x7FFFFFFF || (causal != 0 && causal != 1) || max_seqlen_q < 0)
+  if (h_q < 1 || h_q >= (1 << 20) || h_q % cache->h_kv != 0 || batch < 0 || batch > (1 << 28) || max_blocks < 1)
+    return SMLA_ERR_INVALID_ARGUMENT;
+  if (total_q < 0 || total_q > 0x7FFFFFFF || total_q * h_q > 0x7FFFFFFF || (causal != 0 && causal != 1) ||
+      max_seqlen_q < 0)
     return SMLA_ERR_INVALID_ARGUMENT;
   if (!cu_seqlens_q && (s_q < 0 || (int64_t)batch * s_q != total_q)) return SMLA_ERR_INVALID_ARGUMENT;
   if (!(softcap >= 0.f) || std::isinf(softcap) || std::isinf(softmax_scale)) return SMLA_ERR_INVALID_ARGUMENT;
@@ -216,6 +220,7 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   p.h_q = h_q;
   p.h_kv = cache->h_kv;
   p.group = h_q / cache->h_kv;
+  p.inv_group = 1.0f / (float)p.group;
   p.d = cache->head_dim;
   p.causal = causal;
   p.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)cache->head_dim);
@@ -236,7 +241,9 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   uint8_t* ws = static_cast<uint8_t*>(workspace_ptr);
   smla::Q8Scratch scratch;
   scratch.o = reinterpret_cast<float*>(ws);
+  scratch.cta_o = reinterpret_cast<float*>(ws + wl.cta_o_off);
   scratch.lse = reinterpret_cast<float*>(ws + wl.lse_off);
+  scratch.cta_lse = reinterpret_cast<float*>(ws + wl.cta_lse_off);
   scratch.meta = reinterpret_cast<int32_t*>(ws + wl.meta_off);
   const cudaError_t e = smla::launch_q8_decode(p, int8, max_seqlen_q * p.group, k_map, v_map, scratch, sms,
                                                static_cast<cudaStream_t>(stream));

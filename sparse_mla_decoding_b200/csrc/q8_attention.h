@@ -13,17 +13,18 @@ namespace smla {
 
 constexpr int kQ8DecodeWarps = 12;       // most warps of a CTA, each with its own range of the work
 constexpr int kQ8PartRows = 16;          // rows of a partial
-constexpr int64_t kQ8MinVisits = 2;      // least blocks of a warp's range
+constexpr int64_t kQ8MinVisits = 4;      // least blocks of a CTA's range
 
 // Rows (tokens times the head group) of a request up to which the decode kernel
 // runs: it reads the cache once per 16 rows.
 constexpr int64_t kQ8DecodeRows = 32;
 
-// Partials of the decode kernel: two slots of kQ8PartRows rows for each warp.
+// Partials of the decode kernel: two slots of kQ8PartRows rows for each warp and for
+// each CTA.
 struct Q8Scratch {
-  float* o;                              // [2 parts][kQ8PartRows][d], normalised
-  float* lse;                            // [2 parts][kQ8PartRows], log2
-  int32_t* meta;                         // [parts][8]: the unit a part begins inside
+  float *o, *cta_o;                      // [2 warps or CTAs][kQ8PartRows][d], normalised
+  float *lse, *cta_lse;                  // [2 warps or CTAs][kQ8PartRows], log2
+  int32_t* meta;                         // [CTAs][8]: the unit that a CTA's range begins inside
 };
 
 // `rows`: the most rows (tokens times the head group) of a request, as far as the

@@ -38,6 +38,7 @@ struct Q8Params {
   const int32_t* docs;            // [total_q][2] or NULL
   int max_blocks, batch, s_q, total_q, h_q, h_kv, group, d;
   int causal;
+  float inv_group;                // 1 / group
   float scale;                    // softmax scale
   float cap;                      // 0: none
   float cap_log2, inv_cap_log2;   // cap log2(e) and its inverse
@@ -170,54 +171,35 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// tanh for score caps.  |x| <= 0.75: x P(x^2), P a degree-5 fit to tanh(x)/x in
-// relative error (1.6e-7 in fp32, fitted by reweighted least squares on
-// Chebyshev nodes), so a small score keeps its relative precision; larger |x|:
-// 1 - 2 / (1 + exp(2|x|)) with the sign of x.
-constexpr float kTanhSmall = 0.75f;
-__device__ __forceinline__ float tanh_small(float x) {
-  const float z = x * x;
-  float r = -0.004716585855931044f;
-  r = fmaf(r, z, 0.01958341710269451f);
-  r = fmaf(r, z, -0.0533447191119194f);
-  r = fmaf(r, z, 0.13325412571430206f);
-  r = fmaf(r, z, -0.33332958817481995f);
-  r = fmaf(r, z, 1.0f);
-  return r * x;
-}
-__device__ __forceinline__ float2 tanh_small2(float2 x) {
-  const float2 z = mul2(x, x);
-  float2 r = fma2(both(-0.004716585855931044f), z, both(0.01958341710269451f));
-  r = fma2(r, z, both(-0.0533447191119194f));
-  r = fma2(r, z, both(0.13325412571430206f));
-  r = fma2(r, z, both(-0.33332958817481995f));
-  r = fma2(r, z, both(1.0f));
-  return mul2(r, x);
-}
-__device__ __forceinline__ float tanh_full(float x) {
-  const float a = fabsf(x);
-  float rc;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(1.f + ex2(a * (2.f * kLog2e))));
-  const float big = copysignf(fmaf(-2.f, rc, 1.f), x);
-  return a <= kTanhSmall ? tanh_small(x) : big;
-}
-
-// x_j = cap tanh(x_j fc) of n scores: where a warp has only small ones, by the
-// polynomial alone (one vote for the n scores).
+// x_j = cap tanh(x_j fc) of N scores; one vote of the warp for the N picks the way.
+// All |x| <= 0.75: x P(x^2), P a degree-5 fit to tanh(x)/x in relative error (1.6e-7
+// in fp32; reweighted least squares on Chebyshev nodes), so small scores keep their
+// relative precision and no special function is used.  Else 1 - 2 / (1 + exp(2 |x|))
+// with the sign of x, off by some 1e-7 of the cap.
 template <int N>
 __device__ __forceinline__ void cap_scores(float* x, float fc, float cap) {
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < N; j += 2) top = max3(top, fabsf(x[j]), fabsf(x[j + 1]));
-  if (__any_sync(0xffffffffu, !(top * fc <= kTanhSmall))) {
+  if (__any_sync(0xffffffffu, !(top * fc <= 0.75f))) {
+    const float fe = fc * (2.f * kLog2e);
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = cap * tanh_full(x[j] * fc);
+    for (int j = 0; j < N; ++j) {
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(fabsf(x[j]) * fe)));
+      x[j] = copysignf(fmaf(-2.f * cap, r, cap), x[j]);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
-      const float2 y = mul2(tanh_small2(mul2(make_float2(x[j], x[j + 1]), both(fc))), both(cap));
-      x[j] = y.x;
-      x[j + 1] = y.y;
+      const float2 y = mul2(make_float2(x[j], x[j + 1]), both(fc)), z = mul2(y, y);
+      float2 r = fma2(both(-0.004716585855931044f), z, both(0.01958341710269451f));
+      r = fma2(r, z, both(-0.0533447191119194f));
+      r = fma2(r, z, both(0.13325412571430206f));
+      r = fma2(r, z, both(-0.33332958817481995f));
+      r = mul2(fma2(r, z, both(1.0f)), mul2(y, both(cap)));
+      x[j] = r.x;
+      x[j + 1] = r.y;
     }
   }
 }

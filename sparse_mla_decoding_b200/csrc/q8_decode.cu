@@ -10,10 +10,12 @@
 // Work: one visit is one cache block of one (request, row tile, KV head); the rows
 // of a tile are (token, head of the group) pairs, so a block's codes are read once
 // for the whole group.  All visits, in (request, row tile, head, block) order, are
-// cut into equal ranges, one per warp; a warp walks its range alone, with its own
-// ring of TMA tiles, and no warp waits for another.  A range that holds a whole
-// (request, tile, head) writes o itself; pieces of one go to the workspace as
-// normalised partials that q8_combine_kernel merges by their lse.
+// cut into equal ranges, one per CTA, and those into one per warp; a warp walks its
+// range alone, with its own ring of TMA tiles, and no warp waits for another.  A
+// range that holds a whole (request, tile, head) writes o itself; pieces of one are
+// normalised partials in the workspace.  When its warps are done a CTA merges the
+// pieces that it has of each unit (by their lse), so at most two partials a CTA are
+// left for q8_combine_kernel.
 //
 // Products: S^T = K Q^T and O^T = V^T P^T on m16n8k16, so the cache's codes fill
 // the 16-row side and a tile has 8 rows (one MMA column block) or 16 (two): a group
@@ -28,10 +30,14 @@
 // takes the factor out again per block.  P is rounded to f16 once (2^-11).
 //
 // Bound by HBM: d + 1/16 bytes a key, value and head; what has to keep up is the
-// conversion, about 470 instructions a warp and block (16 KB at d = 128).
+// conversion, about 470 instructions a warp and block (16 KB at d = 128).  What costs
+// beside it is code that runs once: a step of decoding reads more than L2 holds, so
+// each launch fetches its instructions from memory again.  Every part is therefore
+// kept to one copy (at 140 KB of code, merging a few rows took 11000 clocks).
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "q8_attention.h"
 #include "q8_cache.h"
@@ -54,10 +60,15 @@ constexpr int kWarpsOf = NT == 1 ? 12 : 8;
 template <int D, int NT>
 constexpr int kTileSlots = 192 * 1024 / (kBlk * D * kWarpsOf<NT>);
 
-struct Entry {                            // one visit of the ring
+// One visit, as the loading side leaves it for the computing one.
+struct Entry {
   int block, head;                        // cache block (-1: nothing to read) and KV head
   float k_scale, v_scale;
+  int blk, rt;                            // block of the request, row tile
+  int ends;                               // bits: first and last visit of its unit
+  int request;                            // slot of its request's Work
 };
+constexpr int kRequests = 8;              // requests whose Work a warp keeps (a batch of entries has one)
 
 // Blocks [first, first + count) that any row of the request sees; at least one,
 // so that every request with new tokens gets its outputs written.
@@ -85,56 +96,20 @@ __device__ __forceinline__ int row_tiles(const Q8Params& p, int n) {
   return (n * p.group + 8 * NT - 1) / (8 * NT);
 }
 
-template <int NT>
-__device__ __forceinline__ int64_t visits_of(const Q8Params& p, int r) {
-  bool bad;
-  const Q8Request x = q8_request(p, r, &bad);
-  if (x.n == 0) return 0;
-  int first, count;
-  block_span(p, x, first, count);
-  return (int64_t)p.h_kv * row_tiles<NT>(p, x.n) * count;
-}
-
-// A position in the list of visits.
-template <int NT>
-struct Cursor {
-  int r;
+// A request's share of the list of visits: units (row tile, KV head) of `count` blocks.
+struct Work {
   Q8Request x;
-  int first, count, units, unit, blk;
-
-  __device__ __forceinline__ void load(const Q8Params& p) {
-    bool bad;
-    x = q8_request(p, r, &bad);
-    block_span(p, x, first, count);
-    units = p.h_kv * row_tiles<NT>(p, x.n);
-  }
-  // to visit `off` of the requests from r on
-  __device__ __forceinline__ void seek(const Q8Params& p, int64_t off) {
-    while (true) {
-      load(p);
-      const int64_t have = (int64_t)units * count;
-      if (off < have) break;
-      off -= have;
-      ++r;
-    }
-    unit = (int)(off / count);
-    blk = (int)(off % count);
-  }
-  __device__ __forceinline__ void next_request(const Q8Params& p) {
-    do {
-      ++r;
-      if (r >= p.batch) return;
-      load(p);
-    } while (units == 0);
-    unit = blk = 0;
-  }
-  __device__ __forceinline__ void step(const Q8Params& p) {
-    if (++blk < count) return;
-    blk = 0;
-    if (++unit < units) return;
-    next_request(p);
-  }
+  int first, count, units;
 };
+
+template <int NT>
+__device__ __forceinline__ Work work_of(const Q8Params& p, int r, bool* bad) {
+  Work w;
+  w.x = q8_request(p, r, bad);
+  block_span(p, w.x, w.first, w.count);
+  w.units = p.h_kv * row_tiles<NT>(p, w.x.n);
+  return w;
+}
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
@@ -155,6 +130,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 4 bytes to shared memory, without waiting for them.
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // 8 x 8 f16 values, a row's pairs by its four lanes, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t t;
@@ -162,13 +142,34 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return t;
 }
 
+// What a warp holds of a unit that it does not hold whole: of the one that its range
+// begins inside (head), and of the one that it begins and does not end (tail).
+struct Piece {
+  int there, ends;                        // it exists; the unit ends in it
+  int q0, n, head, rt;
+};
+
+// Where a warp's loading side stands: its request, and the visit (unit, blk) of it that
+// the next batch of entries starts with.  Kept in shared memory: it is used once in
+// 32 visits, and the registers are the accumulators'.
+struct Loader {
+  Work work;
+  int r, unit, blk, batches;
+  uint32_t skip;                          // visits from the start of request r to the range's
+};
+
 template <int D, int NT>
 struct Shared {                           // at a 1024-byte boundary: the tiles' swizzle pattern
   uint8_t tile[kWarpsOf<NT>][kTileSlots<D, NT>][kBlk * D];
   Entry ring[kWarpsOf<NT>][kRing];
+  Work request[kWarpsOf<NT>][kRequests];
   uint64_t full[kWarpsOf<NT>][kTileSlots<D, NT>];
-  int64_t before[kWarpsOf<NT> * 32 + 1];  // visits before each thread's requests
+  uint32_t before[kWarpsOf<NT> * 32];     // visits before each thread's requests
   int64_t warp_sum[kWarpsOf<NT>];
+  Piece head[kWarpsOf<NT>], tail[kWarpsOf<NT>];
+  Loader loader[kWarpsOf<NT>];
+  float2 bias[kWarpsOf<NT>][8 * NT];      // of a row: position, and slope in base 2
+  int2 sees[kWarpsOf<NT>][8 * NT];        // positions that a row sees
 };
 
 template <int D, int NT>
@@ -181,6 +182,90 @@ __device__ __forceinline__ bool tile_ready(uint64_t* bar, uint32_t phase, uint32
 }
 
 }  // namespace
+
+// The merge of normalised pieces of a row by eight lanes, against a running maximum:
+// a lane's values are d = 32 k + 4 (lane % 8) and the next three.  A piece is one trip
+// to L2 (some thousand clocks while other CTAs still stream), so a warp takes four rows
+// at once and has four pieces of each under way.
+template <int D>
+struct Merged {
+  static constexpr int kV = D / 32, kAtOnce = 4;
+  float top = -INFINITY, sum = 0.f;
+  float4 o[kV];
+
+  __device__ __forceinline__ Merged() {
+#pragma unroll
+    for (int k = 0; k < kV; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  static __device__ __forceinline__ void axpy(float4& y, float a, const float4& x) {
+    y.x = fmaf(a, x.x, y.x);
+    y.y = fmaf(a, x.y, y.y);
+    y.z = fmaf(a, x.z, y.z);
+    y.w = fmaf(a, x.w, y.w);
+  }
+
+  // Pieces from, from + step, .. last; piece q is in slot 2q, the first of a unit that
+  // begins in it in slot 2q + 1.
+  __device__ __forceinline__ void add(const float* po, const float* plse, int from, int last, int step, int begins,
+                                      int row, int lane8) {
+#pragma unroll 1
+    for (int p0 = from; p0 <= last; p0 += step * kAtOnce) {
+      float lse[kAtOnce];
+      float4 x[kAtOnce][kV];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int q = min(p0 + j * step, last);       // past the last: read it again, with no weight
+        const int64_t at = ((int64_t)2 * q + (q == begins ? 1 : 0)) * kPartRows + row;
+        lse[j] = plse[at];
+#pragma unroll
+        for (int k = 0; k < kV; ++k) x[j][k] = reinterpret_cast<const float4*>(po + at * D)[8 * k + lane8];
+        if (p0 + j * step > last) lse[j] = -INFINITY;
+      }
+      float now = top;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) now = fmaxf(now, lse[j]);
+      const float keep = now == -INFINITY ? 1.f : ex2(top - now);
+      top = now;
+      sum *= keep;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (lse[j] == -INFINITY) continue;
+        const float w = ex2(lse[j] - now);
+        sum += w;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) axpy(o[k], w, x[j][k]);
+      }
+    }
+  }
+  __device__ __forceinline__ float inverse() const { return sum == 0.f ? 0.f : 1.f / sum; }
+  __device__ __forceinline__ float lse2() const { return sum == 0.f ? -INFINITY : top + log2f(sum); }
+
+  // row `row` of the request's rows: o and lse
+  __device__ __forceinline__ void store(const Q8Params& p, int q0, int head, int row, int lane8) const {
+    const int t = row / p.group, hq = head * p.group + row - t * p.group;
+    const int64_t at = (int64_t)(q0 + t) * p.h_q + hq;
+    const float inv = inverse();
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      __nv_bfloat162 a = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
+      __nv_bfloat162 b = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
+      reinterpret_cast<uint2*>(p.o + at * D)[8 * k + lane8] =
+          make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+    }
+    if (lane8 == 0) p.lse[at] = lse2() * kLn2;
+  }
+  // as a piece
+  __device__ __forceinline__ void keep(float* po, float* plse, int64_t at, int lane8) const {
+    const float inv = inverse();
+#pragma unroll
+    for (int k = 0; k < kV; ++k)
+      reinterpret_cast<float4*>(po + at * D)[8 * k + lane8] =
+          make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv);
+    if (lane8 == 0) plse[at] = lse2();
+  }
+};
 
 // One warp: thread (g, c) = (lane / 4, lane % 4).  K codes: thread c takes d in [32c,
 // 32c + 32) (16c at d = 64) of keys 16i + g and 16i + g + 8, so the MMA's k indices
@@ -212,13 +297,14 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
   // Visits before each thread's share of the requests.
   const int share = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
   int64_t mine = 0;
+#pragma unroll 1
   for (int r = tid * share; r < min(p.batch, (tid + 1) * share); ++r) {
-    mine += visits_of<NT>(p, r);
+    bool bad;
+    const Work w = work_of<NT>(p, r, &bad);
+    mine += (int64_t)w.units * w.count;
     if (blockIdx.x == 0) {
-      bool bad;
-      const Q8Request x = q8_request(p, r, &bad);
       if (bad) report_status(p.status, kStatusBadSchedule);
-      if (x.n > 0 && (x.len + kBlk - 1) / kBlk > p.max_blocks) report_status(p.status, kStatusBadBlockTable);
+      if (w.x.n > 0 && (w.x.len + kBlk - 1) / kBlk > p.max_blocks) report_status(p.status, kStatusBadBlockTable);
     }
   }
   int64_t incl = mine;
@@ -230,167 +316,139 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
   if (lane == 31) sm.warp_sum[warp] = incl;
   mbar_init_fence();
   __syncthreads();
-  int64_t base = 0, total = 0;
-#pragma unroll
+  int64_t base = 0, all = 0;
+#pragma unroll 1
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) base += sm.warp_sum[w];
-    total += sm.warp_sum[w];
+    all += sm.warp_sum[w];
   }
-  sm.before[tid] = base + incl - mine;
-  if (tid == 0) sm.before[kWarps * 32] = total;
+  sm.before[tid] = (uint32_t)(base + incl - mine);
   __syncthreads();
+  // 2^31 blocks are tens of TB to read: lengths that ask for more are not meant
+  const uint32_t total = all < 0x7FFFFFFF ? (uint32_t)all : 0u;
+  if (all >= 0x7FFFFFFF && blockIdx.x == 0 && tid == 0) report_status(p.status, kStatusBadSchedule);
 
-  const int parts = gridDim.x * kWarps;
-  const int part = warp * gridDim.x + blockIdx.x;   // neighbours in the list go to different SMs
-  int64_t len = (total + parts - 1) / parts;
-  if (len < kQ8MinVisits) len = kQ8MinVisits;
-  const int64_t v0 = part * len, v1 = min(v0 + len, total);
-  int* meta = scratch.meta + (size_t)part * 8;
-  if (v0 >= v1) {
-    if (lane == 0) meta[0] = 0;
-    return;
-  }
-  Cursor<NT> cur;
-  {
-    int lo = 0, hi = kWarps * 32 - 1;               // the last share that starts at or before v0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (sm.before[mid] <= v0) lo = mid;
-      else hi = mid - 1;
-    }
-    cur.r = lo * share;
-    cur.seek(p, v0 - sm.before[lo]);
-  }
-  const int visits = (int)(v1 - v0);
+  // The CTA's range of visits, and the warp's of it.
+  const uint32_t cta_len = max((total + gridDim.x - 1) / gridDim.x, (uint32_t)kQ8MinVisits);
+  const uint32_t len = (cta_len + kWarps - 1) / kWarps;
+  const uint32_t c0 = min(blockIdx.x * cta_len, total), c1 = min(c0 + cta_len, total);
+  const uint32_t v0 = min(c0 + warp * len, c1), v1 = min(v0 + len, c1);
+  const int part = blockIdx.x * kWarps + warp, visits = (int)(v1 - v0);
+  if (lane == 0) sm.head[warp].there = sm.tail[warp].there = 0;
+  if (tid == 0) scratch.meta[(size_t)blockIdx.x * 8] = 0;
   Entry* ring = sm.ring[warp];
   uint64_t* full = sm.full[warp];
   const uint32_t tiles = smem_u32(&sm.tile[warp][0][0]);
 
-  // The loading side runs ahead of the computing one by the ring's tiles.  It
-  // reads the table and the scales of up to 32 visits of a request at a time.
-  Cursor<NT> ahead = cur;
-  int known = 0;                                    // visits whose entries are in the ring
+  int known = 0;                                    // visits that have entries
+  if (visits > 0) {
+    int n = 0;                                      // shares that start at or before v0
+#pragma unroll 1
+    for (int i = 0; i < kWarps; ++i) n += sm.before[32 * i + lane] <= v0 ? 1 : 0;
+    n = __reduce_add_sync(0xffffffffu, n) - 1;      // the last of them (empty ones before it start there too)
+    if (lane == 0) {
+      Loader& at = sm.loader[warp];
+      at.work.units = at.unit = at.blk = at.batches = 0;
+      at.r = n * share - 1;
+      at.skip = v0 - sm.before[n];
+    }
+    __syncwarp();
+  }
+  // A batch of entries: up to 32 visits of one request.
   auto fill_ring = [&]() {
-    const int64_t left = (int64_t)(ahead.units - ahead.unit) * ahead.count - ahead.blk;
-    const int m = (int)min((int64_t)min(32, visits - known), left);
+    Loader& state = sm.loader[warp];
+    Work ahead = state.work;
+    int r = state.r, unit = state.unit, blk = state.blk;
+    const int batches = state.batches;
+    uint32_t skip = state.skip;
+    while (unit >= ahead.units) {                   // the next request that has visits
+      ++r;
+      bool bad;
+      ahead = work_of<NT>(p, r, &bad);
+      const uint32_t have = (uint32_t)ahead.units * (uint32_t)ahead.count, jump = min(skip, have);
+      skip -= jump;
+      unit = (int)(jump / (uint32_t)ahead.count);
+      blk = (int)(jump - (uint32_t)unit * (uint32_t)ahead.count);
+    }
+    const uint32_t left = (uint32_t)(ahead.units - unit) * (uint32_t)ahead.count - (uint32_t)blk;
+    const int m = (int)min((uint32_t)min(32, visits - known), left);
+    if (lane == 0) sm.request[warp][batches % kRequests] = ahead;
+    const uint32_t at = (uint32_t)(blk + lane), up = at / (uint32_t)ahead.count, in_unit = at - up * ahead.count;
     if (lane < m) {
-      const int at = ahead.blk + lane;
-      const int unit = ahead.unit + at / ahead.count;
-      const int blk = ahead.first + at % ahead.count;
-      Entry e{-1, unit % p.h_kv, 0.f, 0.f};
-      if (blk < p.max_blocks && blk * (int64_t)kBlk < ahead.x.len) {
-        const int page = p.block_table[(int64_t)ahead.r * p.max_blocks + blk];
-        if (page >= 0 && page < p.num_blocks) {
-          e.block = page;
-          e.k_scale = p.k_scale[page * p.k_scale_stride + e.head];
-          e.v_scale = p.v_scale[page * p.v_scale_stride + e.head];
-        } else {
+      const int u = unit + (int)up, rt = u / p.h_kv, head = u - rt * p.h_kv, b = ahead.first + (int)in_unit;
+      Entry& e = ring[(known + lane) % kRing];
+      int page = -1;
+      if (b < p.max_blocks && b * (int64_t)kBlk < ahead.x.len) {
+        page = p.block_table[(int64_t)r * p.max_blocks + b];
+        if (page < 0 || page >= p.num_blocks) {
           report_status(p.status, kStatusBadBlockTable);
+          page = -1;
         }
       }
-      ring[(known + lane) % kRing] = e;
+      e.block = page;
+      e.head = head;
+      e.blk = b;
+      e.rt = rt;
+      e.ends = (in_unit == 0 ? 1 : 0) | ((int)in_unit + 1 == ahead.count ? 2 : 0);
+      e.request = batches % kRequests;
+      if (page >= 0) {                              // the copies of the tiles need not wait for these
+        copy4(&e.k_scale, p.k_scale + page * p.k_scale_stride + head);
+        copy4(&e.v_scale, p.v_scale + page * p.v_scale_stride + head);
+      }
+    }
+    // For the combine kernel: which CTAs share the unit that this CTA's range begins inside.
+    if (known == 0 && warp == 0 && lane == 0 && blk > 0) {
+      int* meta = scratch.meta + (size_t)blockIdx.x * 8;
+      const uint32_t u0 = v0 - (uint32_t)blk;
+      meta[0] = 1;
+      meta[1] = (int)(u0 / cta_len);
+      meta[2] = (int)((u0 + (uint32_t)ahead.count - 1) / cta_len);
+      meta[3] = ahead.x.q0;
+      meta[4] = ahead.x.n;
+      meta[5] = unit % p.h_kv;
+      meta[6] = unit / p.h_kv;
     }
     known += m;
-    const int64_t at = ahead.blk + m;
-    ahead.unit += (int)(at / ahead.count);
-    ahead.blk = (int)(at % ahead.count);
-    if (ahead.unit >= ahead.units && known < visits) ahead.next_request(p);
+    __syncwarp();
+    if (lane == 0) {
+      const uint32_t next = (uint32_t)(blk + m), over = next / (uint32_t)ahead.count;
+      state = {ahead, r, unit + (int)over, (int)(next - over * (uint32_t)ahead.count), batches + 1, skip};
+    }
     __syncwarp();
   };
-  auto issue = [&](int tile, int slot) {            // tile 2v: keys of visit v, 2v + 1: values
+  // tile 2v: keys of visit v, 2v + 1: values
+  auto issue = [&](int tile, int slot) {
     const int v = tile >> 1;
-    if (v >= visits) return;
-    while (v >= known) fill_ring();
-    if (lane == 0) {
-      const Entry e = ring[v % kRing];
-      if (e.block >= 0) {
+    if (v < visits && lane == 0) {
+      const int block = ring[v % kRing].block, head = ring[v % kRing].head;
+      if (block >= 0) {
         mbar_arrive_tx(&full[slot], kBlk * D);
-        tma_tile(tiles + slot * (kBlk * D), (tile & 1) ? &v_map : &k_map, e.head, e.block, &full[slot]);
+        tma_tile(tiles + slot * (kBlk * D), (tile & 1) ? &v_map : &k_map, head, block, &full[slot]);
       } else {
         mbar_arrive1(&full[slot]);
       }
     }
   };
-  for (int i = 0; i < kSlots; ++i) issue(i, i);
 
   uint32_t Q[NT][kSteps][2];
   float O[NT][kOut][4];
-  // of rows 2c and 2c + 1 of each column block: power of two of q, softmax state, visibility
-  float row_fac[NT][2], m[NT][2], l[NT][2], slope[NT][2], pos[NT][2];
-  int lo[NT][2], hi[NT][2], all_lo = 0, all_hi = 0;
+  // of rows 2c and 2c + 1 of each column block: power of two of q, softmax state
+  float row_fac[NT][2], m[NT][2], l[NT][2];
+  int all_lo = 0, all_hi = 0;                       // what every row of the tile sees
   float base_log2 = 0.f;
   bool opened = false;                              // base_log2 is set
   const float sl2 = p.scale * kLog2e;
-
-  auto open_unit = [&]() {
-    const int head = cur.unit % p.h_kv, rt = cur.unit / p.h_kv;
-    opened = false;
-    all_lo = 0;
-    all_hi = 0x7FFFFFFF;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      {                                             // q of row 8 nt + g
-        const int row = rt * kRows + 8 * nt + g, t = row / p.group, hq = head * p.group + row % p.group;
-        uint4 w[kPer / 8];
-#pragma unroll
-        for (int k = 0; k < kPer / 8; ++k) w[k] = make_uint4(0, 0, 0, 0);
-        if (t < cur.x.n) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(cur.x.q0 + t) * p.q_token_stride +
-                                                            (int64_t)hq * p.q_head_stride + kPer * c);
-#pragma unroll
-          for (int k = 0; k < kPer / 8; ++k) w[k] = __ldg(src + k);
-        }
-        auto lo_of = [](uint32_t v) { return __uint_as_float(v << 16); };
-        auto hi_of = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
-        float top = 0.f;
-#pragma unroll
-        for (int k = 0; k < kPer / 8; ++k) {
-          const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = max3(top, fabsf(lo_of(u[j])), fabsf(hi_of(u[j])));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        float up, down;
-        row_pow2(top, up, down);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) row_fac[nt][i] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + i));
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const uint4 a = w[s >> 1];
-          const uint32_t x = s & 1 ? a.z : a.x, y = s & 1 ? a.w : a.y;
-          Q[nt][s][0] = pack_f16(lo_of(x) * up, hi_of(x) * up);
-          Q[nt][s][1] = pack_f16(lo_of(y) * up, hi_of(y) * up);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = rt * kRows + 8 * nt + 2 * c + i, t = row / p.group, hq = head * p.group + row % p.group;
-        m[nt][i] = -INFINITY;
-        l[nt][i] = 0.f;
-        lo[nt][i] = 0;
-        hi[nt][i] = 0x7FFFFFFF;
-        slope[nt][i] = 0.f;
-        pos[nt][i] = (float)(cur.x.len - cur.x.n + t);
-        if (t < cur.x.n) {
-          q8_visible(p, cur.x, t, lo[nt][i], hi[nt][i]);
-          if (p.slopes) slope[nt][i] = p.slopes[hq] * kLog2e;
-          all_lo = max(all_lo, lo[nt][i]);
-          all_hi = min(all_hi, hi[nt][i]);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < kOut; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) O[nt][t][k] = 0.f;
-    }
-    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+  // Token of row j of row tile rt, and its head in the group.  The division by the
+  // group is by its inverse: exact below 2^20.
+  auto token_of = [&](int rt, int j, int& in_group) {
+    const int t0 = rt * kRows / p.group, h = rt * kRows - t0 * p.group + j;
+    const int up = __float2int_rz(((float)h + 0.5f) * p.inv_group);
+    in_group = h - up * p.group;
+    return t0 + up;
   };
 
   // The unit's result, or this warp's piece of it.
-  auto close_unit = [&](bool whole, bool begun_here) {
-    const int head = cur.unit % p.h_kv, rt = cur.unit / p.h_kv;
+  auto close_unit = [&](const Entry& e, const Q8Request& x, bool whole, bool begun_here) {
     const float back = ex2(base_log2);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -402,12 +460,13 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
         s += __shfl_xor_sync(0xffffffffu, s, 16);
         const float inv = s == 0.f ? 0.f : back / s;
         const float lse2 = s == 0.f ? -INFINITY : m[nt][i] + log2f(s);
-        const int in_tile = 8 * nt + 2 * c + i, row = rt * kRows + in_tile, t = row / p.group;
-        const int hq = head * p.group + row % p.group;
-        if (t >= cur.x.n) continue;
+        const int in_tile = 8 * nt + 2 * c + i;
+        int hh;
+        const int t = token_of(e.rt, in_tile, hh), hq = e.head * p.group + hh;
+        if (t >= x.n) continue;
         // rows g and g + 8 of output tile k: d = kCols g + 2k and + 1
         if (whole) {
-          const int64_t at = (int64_t)(cur.x.q0 + t) * p.h_q + hq;
+          const int64_t at = (int64_t)(x.q0 + t) * p.h_q + hq;
           uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + kCols * g);
 #pragma unroll
           for (int k = 0; k < kOut / 4; ++k) {
@@ -432,28 +491,95 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
       }
   };
 
-  // Which parts share the unit this range begins inside, for the merge.
-  if (lane == 0) {
-    meta[0] = cur.blk > 0 ? 1 : 0;
-    if (cur.blk > 0) {
-      const int64_t u0 = v0 - cur.blk;
-      meta[1] = (int)(u0 / len);
-      meta[2] = (int)((u0 + cur.count - 1) / len);
-      meta[3] = cur.x.q0;
-      meta[4] = cur.x.n;
-      meta[5] = cur.unit % p.h_kv;
-      meta[6] = cur.unit / p.h_kv;
-    }
-  }
-
-  int slot = 0;
+  constexpr int kLead = (kSlots + 1) / 2;           // visits that the ring of tiles runs ahead
+  int slot = 0, v = 0;
   uint32_t phase = 0;
-  bool begun_here = cur.blk == 0;
-  open_unit();
-  int v = 0;
+  bool begun_here = false;
   for (; v < visits; ++v) {
-    const Entry e = ring[v % kRing];
-    const int j0 = (cur.first + cur.blk) * kBlk;
+    while (known < min(visits, v + 1 + kLead)) fill_ring();
+    if (v == 0) {
+#pragma unroll 1
+      for (int i = 0; i < kSlots; ++i) issue(i, i);
+    }
+    const int ends = ring[v % kRing].ends;
+    if (v == 0 || (ends & 1)) {                     // open a unit
+      const int head = ring[v % kRing].head, rt = ring[v % kRing].rt;
+      const Q8Request x = sm.request[warp][ring[v % kRing].request].x;
+      begun_here = ends & 1;
+      opened = false;
+      all_lo = 0;
+      all_hi = 0x7FFFFFFF;
+      uint4 raw_q[NT][kPer / 8];                    // q of row 8 nt + g
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        int hh;
+        const int t = token_of(rt, 8 * nt + g, hh);
+#pragma unroll
+        for (int k = 0; k < kPer / 8; ++k) raw_q[nt][k] = make_uint4(0, 0, 0, 0);
+        if (t < x.n) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(x.q0 + t) * p.q_token_stride +
+                                                            (int64_t)(head * p.group + hh) * p.q_head_stride + kPer * c);
+#pragma unroll
+          for (int k = 0; k < kPer / 8; ++k) raw_q[nt][k] = __ldg(src + k);
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          int hh;
+          const int t = token_of(rt, 8 * nt + 2 * c + i, hh);
+          m[nt][i] = -INFINITY;
+          l[nt][i] = 0.f;
+          int lo = 0, hi = 0x7FFFFFFF;
+          if (t < x.n) {
+            q8_visible(p, x, t, lo, hi);
+            if (p.slopes && g == 0)
+            sm.bias[warp][8 * nt + 2 * c + i] =
+                make_float2((float)(x.len - x.n + t), p.slopes[head * p.group + hh] * kLog2e);
+            all_lo = max(all_lo, lo);
+            all_hi = min(all_hi, hi);
+          }
+          if (g == 0) sm.sees[warp][8 * nt + 2 * c + i] = make_int2(lo, hi);
+        }
+#pragma unroll
+        for (int t = 0; t < kOut; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) O[nt][t][k] = 0.f;
+      }
+      all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+      all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+      auto lo_of = [](uint32_t b) { return __uint_as_float(b << 16); };
+      auto hi_of = [](uint32_t b) { return __uint_as_float(b & 0xFFFF0000u); };
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float top = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPer / 8; ++k) {
+          const uint32_t b[4] = {raw_q[nt][k].x, raw_q[nt][k].y, raw_q[nt][k].z, raw_q[nt][k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = max3(top, fabsf(lo_of(b[j])), fabsf(hi_of(b[j])));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float up, down;
+        row_pow2(top, up, down);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) row_fac[nt][i] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + i));
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const uint4 a = raw_q[nt][s >> 1];
+          const uint32_t b0 = s & 1 ? a.z : a.x, b1 = s & 1 ? a.w : a.y;
+          Q[nt][s][0] = pack_f16(lo_of(b0) * up, hi_of(b0) * up);
+          Q[nt][s][1] = pack_f16(lo_of(b1) * up, hi_of(b1) * up);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // the scales of the entries
+    __syncwarp();
+    // at d = 128 read where used: the registers are the accumulators'
+    const std::conditional_t<D == 64, Entry, Entry&> e = ring[v % kRing];
+    const int j0 = e.blk * kBlk;
     // ---- S^T = K Q^T
     if (!tile_ready(&full[slot], phase, p.status)) break;
     float S[NT][4][4];                              // [16 keys][key g: rows 2c, 2c + 1; key g + 8: the same]
@@ -513,12 +639,14 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
             for (int j = 0; j < 8; ++j) S[nt][j >> 1][2 * (j & 1) + i] *= f;
           }
           if (p.slopes) {
-            const float d0 = pos[nt][i] - (float)(j0 + g);
+            const float2 b = sm.bias[warp][8 * nt + 2 * c + i];
+            const float d0 = b.x - (float)(j0 + g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) S[nt][j >> 1][2 * (j & 1) + i] -= slope[nt][i] * fabsf(d0 - (float)(8 * j));
+            for (int j = 0; j < 8; ++j) S[nt][j >> 1][2 * (j & 1) + i] -= b.y * fabsf(d0 - (float)(8 * j));
           }
           if (edge) {
-            const int a = lo[nt][i] - j0 - g, b = hi[nt][i] - j0 - g;
+            const int2 see = sm.sees[warp][8 * nt + 2 * c + i];
+            const int a = see.x - j0 - g, b = see.y - j0 - g;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               if (8 * j < a || 8 * j >= b) S[nt][j >> 1][2 * (j & 1) + i] = -INFINITY;
@@ -576,7 +704,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
     if (!tile_ready(&full[slot], phase, p.status)) break;
     const uint32_t vt = tiles + slot * (kBlk * D);
     if (e.block >= 0) {
-      const int tail = cur.x.len - j0;              // rows from here on are not the request's
+      const int tail = sm.request[warp][e.request].x.len - j0;              // rows from here on are not the request's
       if (tail < kBlk) {                            // P is 0 there, and whatever they hold must not be a NaN
         for (int i = tail * (D / 16) + lane; i < kBlk * (D / 16); i += 32)
           asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vt + 16 * i), "r"(0) : "memory");
@@ -613,14 +741,12 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
     issue(2 * v + 1 + kSlots, slot);
     if (++slot == kSlots) slot = 0, phase ^= 1;
     // ---- the end of a unit, or of the range
-    const bool done = cur.blk + 1 == cur.count;
-    if (done || v + 1 == visits) close_unit(done && begun_here, begun_here);
-    if (v + 1 < visits) {
-      cur.step(p);
-      if (done) {
-        begun_here = true;
-        open_unit();
-      }
+    const bool done = e.ends & 2;
+    if (done || v + 1 == visits) {
+      const Q8Request x = sm.request[warp][e.request].x;
+      close_unit(e, x, done && begun_here, begun_here);
+      if (lane == 0 && !(done && begun_here))
+        (begun_here ? sm.tail : sm.head)[warp] = {1, done ? 1 : 0, x.q0, x.n, e.head, e.rt};
     }
   }
   if (v < visits)                                   // a wait gave up: see the copies in flight out before leaving
@@ -628,53 +754,84 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
       tile_ready(&full[slot], phase, p.status);
       if (++slot == kSlots) slot = 0, phase ^= 1;
     }
+
+  // ---- merge what the CTA has of each unit, the rows of all units over the warps.  A chain of pieces starts at a tail, or at the head of warp 0.
+  __syncthreads();
+  int turn = 0;
+#pragma unroll 1
+  for (int s = -1; s < kWarps; ++s) {
+    const bool begun = s >= 0;
+    const Piece& start = begun ? sm.tail[s] : sm.head[0];
+    if (!start.there) continue;
+    const int first = begun ? s : 0;
+    int last = first;
+    while (last + 1 < kWarps && (begun && last == first ? true : !sm.head[last].ends) && sm.head[last + 1].there) ++last;
+    const bool ended = begun && last == first ? false : sm.head[last].ends != 0;
+    const int rows = min(kRows, start.n * p.group - start.rt * kRows);
+    const int p0 = blockIdx.x * kWarps + first, p1 = blockIdx.x * kWarps + last;
+#pragma unroll 1
+    for (int row0 = 0; row0 < rows; row0 += 4) {
+      const int row = row0 + (lane >> 3);
+      if (turn++ % kWarps != warp || row >= rows) continue;
+      Merged<D> got;
+      got.add(scratch.o, scratch.lse, p0, p1, 1, begun ? p0 : -1, row, lane & 7);
+      if (begun && ended)
+        got.store(p, start.q0, start.head, start.rt * kRows + row, lane & 7);
+      else
+        got.keep(scratch.cta_o, scratch.cta_lse, (2 * (int64_t)blockIdx.x + (begun ? 1 : 0)) * kPartRows + row,
+                 lane & 7);
+    }
+  }
 }
 
-// Merges the pieces of a unit.  Part p whose range begins inside a unit that
-// parts first .. last share merges the rows p - first - 1 + k (last - first).
+// Merges what the CTAs have of a unit.  CTA c of the decode whose range begins inside
+// a unit that CTAs first .. last share merges the rows c - first - 1 + k (last -
+// first), so a long request's pieces are merged by as many CTAs as it has rows: eight
+// lanes a row, or with a single row its pieces over all lanes.
+constexpr int kCombineWarps = 4;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(128) q8_combine_kernel(const __grid_constant__ Q8Params p, Q8Scratch scratch) {
-  __shared__ float acc[4][D];
-  __shared__ float wsum[4];
-  const int part = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(32 * kCombineWarps) q8_combine_kernel(const __grid_constant__ Q8Params p,
+                                                                        Q8Scratch scratch) {
+  constexpr int kRows = 8 * NT, kV = D / 32, kTeams = 4 * kCombineWarps;   // teams of eight lanes
+  __shared__ float4 s_o[kTeams][D / 4];
+  __shared__ float s_lse[kTeams];
+  const int lane8 = threadIdx.x & 7, team = threadIdx.x >> 3;
   pdl_wait_primary();
-  const int* meta = scratch.meta + (size_t)part * 8;
-  if (meta[0] == 0) return;
-  const int first = meta[1], last = meta[2], n = meta[4], rt = meta[6];
-  constexpr int kRows = 8 * NT;
-  const int rows = min(kRows, n * p.group - rt * kRows);
-  constexpr int kV = D / 32;
-  for (int row = part - first - 1; row < rows; row += last - first) {
-    auto slot_of = [&](int q) { return (int64_t)2 * q + (q == first ? 1 : 0); };
-    float top = -INFINITY;
-    for (int q = first + lane; q <= last; q += 32) top = fmaxf(top, scratch.lse[slot_of(q) * kPartRows + row]);
+  const int4* meta = reinterpret_cast<const int4*>(scratch.meta + (size_t)blockIdx.x * 8);
+  const int4 ma = meta[0], mb = meta[1];
+  if (ma.x == 0) return;
+  const int first = ma.y, last = ma.z, q0 = ma.w, head = mb.y, rt = mb.z;
+  const int rows = min(kRows, mb.x * p.group - rt * kRows);
+  const int ctas = last - first, idx0 = blockIdx.x - first - 1;
+  if (idx0 >= rows) return;
+  const bool several = idx0 + ctas < rows;            // rows (at most 16: a team each)
+  const int row = several ? idx0 + team * ctas : idx0;
+  Merged<D> got;
+  if (row < rows)
+    got.add(scratch.cta_o, scratch.cta_lse, several ? first : first + team, last, several ? 1 : kTeams, first, row,
+            lane8);
+  if (several) {
+    if (row < rows) got.store(p, q0, head, rt * kRows + row, lane8);
+    return;
+  }
+  const float inv = got.inverse();
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float sum = 0.f, o[kV];
+  for (int k = 0; k < kV; ++k)
+    s_o[team][8 * k + lane8] = make_float4(got.o[k].x * inv, got.o[k].y * inv, got.o[k].z * inv, got.o[k].w * inv);
+  if (lane8 == 0) s_lse[team] = got.lse2();
+  __syncthreads();
+  if (team == 0) {
+    Merged<D> all;
+    for (int w = 0; w < kTeams; ++w) all.top = fmaxf(all.top, s_lse[w]);
+    for (int w = 0; w < kTeams; ++w) {
+      if (s_lse[w] == -INFINITY) continue;
+      const float f = ex2(s_lse[w] - all.top);
+      all.sum += f;
 #pragma unroll
-    for (int k = 0; k < kV; ++k) o[k] = 0.f;
-#pragma unroll 4
-    for (int q = first + warp; q <= last; q += 4) {
-      const int64_t at = slot_of(q) * kPartRows + row;
-      const float lse = scratch.lse[at];
-      const float w = lse == -INFINITY ? 0.f : ex2(lse - top);
-      const float* src = scratch.o + at * D + kV * lane;
-      sum += w;
-#pragma unroll
-      for (int k = 0; k < kV; ++k) o[k] = fmaf(w, src[k], o[k]);
+      for (int k = 0; k < kV; ++k) Merged<D>::axpy(all.o[k], f, s_o[w][8 * k + lane8]);
     }
-    if (lane == 0) wsum[warp] = sum;
-#pragma unroll
-    for (int k = 0; k < kV; ++k) acc[warp][kV * lane + k] = o[k];
-    __syncthreads();
-    const float all = wsum[0] + wsum[1] + wsum[2] + wsum[3];
-    const int idx = rt * kRows + row, t = idx / p.group, hq = meta[5] * p.group + idx % p.group;
-    const int64_t at = (int64_t)(meta[3] + t) * p.h_q + hq;
-    const float inv = all == 0.f ? 0.f : 1.f / all;
-    for (int i = threadIdx.x; i < D; i += 128)
-      p.o[at * D + i] = __float2bfloat16((acc[0][i] + acc[1][i] + acc[2][i] + acc[3][i]) * inv);
-    if (threadIdx.x == 0) p.lse[at] = (top == -INFINITY ? -INFINITY : top + log2f(all)) * kLn2;
-    __syncthreads();
+    all.store(p, q0, head, rt * kRows + row, lane8);
   }
 }
 
@@ -695,8 +852,8 @@ cudaError_t launch(const Q8Params& p, const CUtensorMap& k_map, const CUtensorMa
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(ctas * kWarps));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -139,6 +139,17 @@ def test_many_short_requests():
     check(x)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens", [1, 2])
+def test_ragged_batches_cut_everywhere(tokens, d):
+    """Ranges of CTAs and warps that begin and end at all places of a unit."""
+    rng = np.random.default_rng(d + tokens)
+    lens = np.concatenate([rng.integers(tokens, 200, 30), rng.integers(200, 3000, 12)])
+    rng.shuffle(lens)
+    x = build([tokens] * len(lens), lens, 12, 2, d, "int8", 750 + d + tokens)
+    check(x)
+
+
 def test_four_dimensional_queries_equal_packed_ones():
     x = build([3] * 5, [3, 64, 100, 259, 30], 8, 4, 128, "e4m3", 800)
     o, lse, _ = call(x)
