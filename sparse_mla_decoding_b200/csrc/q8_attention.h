@@ -11,7 +11,7 @@
 
 namespace smla {
 
-constexpr int kQ8DecodeWarps = 12;       // most warps of a CTA, each with its own range of the work
+constexpr int kQ8DecodeWarps = 16;       // most warps of a CTA, each with its own range of the work
 constexpr int kQ8PartRows = 16;          // rows of a partial
 constexpr int64_t kQ8MinVisits = 4;      // least blocks of a CTA's range
 

@@ -49,16 +49,20 @@ namespace smla {
 namespace {
 
 constexpr int kPartRows = kQ8PartRows;    // rows of a partial slot
-constexpr int kRing = 64;                 // visits whose table entries a warp keeps
+constexpr int kBatch = 16;                // visits whose table entries a warp reads at once
+constexpr int kRing = 2 * kBatch;         // and keeps
 constexpr int kSpanTokens = 16;           // document bounds are scanned up to this many new tokens
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-// Warps of a CTA and tiles of a warp's ring: 192 KB of tiles in all.  8 rows take
-// under 170 registers, 16 rows up to 255.
-template <int NT>
-constexpr int kWarpsOf = NT == 1 ? 12 : 8;
+// Warps of a CTA (8 rows take 168 registers at d = 128 and 128 at d = 64, 16 rows up
+// to 255) and tiles of a warp's ring.  About 100 KB of tiles are enough to cover
+// memory's latency, and more in flight is slower: 64 x 8192 tokens at d = 128 took 172
+// us with 12 warps of one tile, 180 with 14 of one, 185 with 12 of two; 37 ragged
+// requests at d = 64 50 us with 16 warps of two tiles, 52 with three, 54 with 12 of four.
 template <int D, int NT>
-constexpr int kTileSlots = 192 * 1024 / (kBlk * D * kWarpsOf<NT>);
+constexpr int kWarpsOf = NT == 2 ? 8 : D == 128 ? 12 : 16;
+template <int D, int NT>
+constexpr int kTileSlots = NT == 1 ? (D == 128 ? 1 : 2) : (D == 128 ? 2 : 3);
 
 // One visit, as the loading side leaves it for the computing one.
 struct Entry {
@@ -151,7 +155,7 @@ struct Piece {
 
 // Where a warp's loading side stands: its request, and the visit (unit, blk) of it that
 // the next batch of entries starts with.  Kept in shared memory: it is used once in
-// 32 visits, and the registers are the accumulators'.
+// a batch, and the registers are the accumulators'.
 struct Loader {
   Work work;
   int r, unit, blk, batches;
@@ -160,20 +164,23 @@ struct Loader {
 
 template <int D, int NT>
 struct Shared {                           // at a 1024-byte boundary: the tiles' swizzle pattern
-  uint8_t tile[kWarpsOf<NT>][kTileSlots<D, NT>][kBlk * D];
-  Entry ring[kWarpsOf<NT>][kRing];
-  Work request[kWarpsOf<NT>][kRequests];
-  uint64_t full[kWarpsOf<NT>][kTileSlots<D, NT>];
-  uint32_t before[kWarpsOf<NT> * 32];     // visits before each thread's requests
-  int64_t warp_sum[kWarpsOf<NT>];
-  Piece head[kWarpsOf<NT>], tail[kWarpsOf<NT>];
-  Loader loader[kWarpsOf<NT>];
-  float2 bias[kWarpsOf<NT>][8 * NT];      // of a row: position, and slope in base 2
-  int2 sees[kWarpsOf<NT>][8 * NT];        // positions that a row sees
+  uint8_t tile[kWarpsOf<D, NT>][kTileSlots<D, NT>][kBlk * D];
+  Entry ring[kWarpsOf<D, NT>][kRing];
+  Work request[kWarpsOf<D, NT>][kRequests];
+  uint64_t full[kWarpsOf<D, NT>][kTileSlots<D, NT>];
+  uint32_t before[kWarpsOf<D, NT> * 32];     // visits before each thread's requests
+  int64_t warp_sum[kWarpsOf<D, NT>];
+  Piece head[kWarpsOf<D, NT>], tail[kWarpsOf<D, NT>];
+  Loader loader[kWarpsOf<D, NT>];
+  float2 bias[kWarpsOf<D, NT>][8 * NT];      // of a row: position, and slope in base 2
+  int2 sees[kWarpsOf<D, NT>][8 * NT];        // positions that a row sees
 };
 
 template <int D, int NT>
 constexpr int kSharedBytes = sizeof(Shared<D, NT>) + 1024;
+static_assert(kSharedBytes<128, 1> <= 232448 && kSharedBytes<64, 1> <= 232448 && kSharedBytes<128, 2> <= 232448 &&
+                  kSharedBytes<64, 2> <= 232448,
+              "227 KB a CTA");
 
 // Whole warp: the phase of `bar` has completed, within the time limit.
 __device__ __forceinline__ bool tile_ready(uint64_t* bar, uint32_t phase, uint32_t* status) {
@@ -275,10 +282,10 @@ struct Merged {
 // in the swizzle of the tiles (two-way for V at d = 64).  The thread holds scores and
 // outputs of rows 2c and 2c + 1 of each column block.
 template <int D, bool kInt8, int NT>
-__global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
+__global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
     q8_decode_kernel(const __grid_constant__ Q8Params p, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, Q8Scratch scratch) {
-  constexpr int kWarps = kWarpsOf<NT>, kRows = 8 * NT;
+  constexpr int kWarps = kWarpsOf<D, NT>, kRows = 8 * NT;
   constexpr int kSlots = kTileSlots<D, NT>;
   constexpr int kSteps = D / 16;          // k-steps of S
   constexpr int kOut = D / 16;            // output tiles
@@ -354,7 +361,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
     }
     __syncwarp();
   }
-  // A batch of entries: up to 32 visits of one request.
+  // A batch of entries: visits of one request.
   auto fill_ring = [&]() {
     Loader& state = sm.loader[warp];
     Work ahead = state.work;
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kWarpsOf<NT> * 32, 1)
       blk = (int)(jump - (uint32_t)unit * (uint32_t)ahead.count);
     }
     const uint32_t left = (uint32_t)(ahead.units - unit) * (uint32_t)ahead.count - (uint32_t)blk;
-    const int m = (int)min((uint32_t)min(32, visits - known), left);
+    const int m = (int)min((uint32_t)min(kBatch, visits - known), left);
     if (lane == 0) sm.request[warp][batches % kRequests] = ahead;
     const uint32_t at = (uint32_t)(blk + lane), up = at / (uint32_t)ahead.count, in_unit = at - up * ahead.count;
     if (lane < m) {
@@ -840,7 +847,7 @@ namespace {
 template <int D, bool kInt8, int NT>
 cudaError_t launch(const Q8Params& p, const CUtensorMap& k_map, const CUtensorMap& v_map, const Q8Scratch& scratch,
                    int ctas, cudaStream_t stream) {
-  constexpr int kWarps = kWarpsOf<NT>, kBytes = kSharedBytes<D, NT>;
+  constexpr int kWarps = kWarpsOf<D, NT>, kBytes = kSharedBytes<D, NT>;
   // per call: the attribute belongs to the current context and costs no launch
   if (const cudaError_t e = cudaFuncSetAttribute(q8_decode_kernel<D, kInt8, NT>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
