@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kTableThreads)
   __shared__ uint64_t warp_tokens[32], warp_blocks[32];
   __shared__ int64_t s_cu[kTableThreads + 1];   // first token of each request
   __shared__ int32_t s_len[kTableThreads], s_first[kTableThreads], s_need[kTableThreads];
-  __shared__ unsigned long long s_taken;
+  __shared__ int s_taken;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t have = min((int64_t)max(num_free[0], 0), free_capacity);
   // this CTA's tokens
@@ -60,11 +60,19 @@ __global__ void __launch_bounds__(kTableThreads)
     __syncthreads();                            // the chunk before is done with the shared arrays
     if (lane == 31) warp_tokens[warp] = t64, warp_blocks[warp] = b64;
     __syncthreads();
-    uint64_t tb = 0, bb = 0, tt = 0, bt = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) tb += warp_tokens[w], bb += warp_blocks[w];
-      tt += warp_tokens[w], bt += warp_blocks[w];
+    if (warp == 0) {                            // inclusive sums over the warps
+      uint64_t t = warp_tokens[lane], b = warp_blocks[lane];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, t, off), z = __shfl_up_sync(0xffffffffu, b, off);
+        if (lane >= off) t += y, b += z;
+      }
+      warp_tokens[lane] = t;
+      warp_blocks[lane] = b;
     }
+    __syncthreads();
+    const uint64_t tb = warp > 0 ? warp_tokens[warp - 1] : 0, bb = warp > 0 ? warp_blocks[warp - 1] : 0;
+    const uint64_t tt = warp_tokens[31], bt = warp_blocks[31];
     const int64_t cu = tokens + (int64_t)(tb + t64) - fresh;
     const int64_t last = blocks + (int64_t)(bb + b64), first = last - max(need, 0);
     const bool fits = need >= 0 && (need == 0 || last <= have) && cu + fresh <= max_new_tokens;
@@ -79,7 +87,8 @@ __global__ void __launch_bounds__(kTableThreads)
         seqlens_out[r] = fits ? len + fresh : len;
         if (r == batch - 1) cu_new[batch] = (int32_t)min(cu + fresh, (int64_t)0x7FFFFFFF);
       }
-      if (fits && need > 0) atomicAdd(&s_taken, (unsigned long long)need);   // integers: order does not matter
+      const int took = __reduce_add_sync(0xffffffffu, fits ? max(need, 0) : 0);   // at most free_capacity in all
+      if (lane == 0 && took > 0) atomicAdd(&s_taken, took);                      // integers: order does not matter
     }
     __syncthreads();
     // table entries: a warp per request, the requests spread over the CTAs
@@ -114,7 +123,7 @@ __global__ void __launch_bounds__(kTableThreads)
   for (int64_t i = max(i0, tokens) + tid; i < i1; i += kTableThreads) slots[i] = -1;   // behind the last token
   if (blockIdx.x == 0) {
     __syncthreads();
-    if (tid == 0) num_free_out[0] = (int32_t)(have - (int64_t)s_taken);
+    if (tid == 0) num_free_out[0] = (int32_t)(have - s_taken);
     if (tid == 0 && batch == 0) cu_new[0] = 0;
   }
 }
@@ -126,7 +135,7 @@ extern "C" int smla_extend_block_table(int32_t* block_table, int max_blocks, con
                                        int64_t free_capacity, const int32_t* num_free, int64_t max_new_tokens,
                                        int64_t* slot_mapping, int32_t* cu_new, int32_t* seqlens_out,
                                        int32_t* num_free_out, void* stream) {
-  if (batch < 0 || max_blocks < 1 || free_capacity < 0 || max_new_tokens < 0 || max_new_tokens > 0x7FFFFFFF)
+  if (batch < 0 || max_blocks < 1 || free_capacity < 0 || free_capacity > 0x7FFFFFFF || max_new_tokens < 0 || max_new_tokens > 0x7FFFFFFF)
     return SMLA_ERR_INVALID_ARGUMENT;
   if (!num_free || !cu_new || !num_free_out || (max_new_tokens > 0 && !slot_mapping) ||
       (free_capacity > 0 && !free_blocks))

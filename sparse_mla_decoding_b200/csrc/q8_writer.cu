@@ -70,26 +70,32 @@ __device__ __forceinline__ float scale_for(float amax) {
 
 }  // namespace
 
+// 64 registers, so that eight CTAs (128 KB of input) are under way on an SM.
 template <int D, bool kInt8>
-__global__ void __launch_bounds__(kThreads) quantize_kv_blocks_kernel(const __grid_constant__ Q8WriteParams p) {
+__global__ void __launch_bounds__(kThreads, 8) quantize_kv_blocks_kernel(const __grid_constant__ Q8WriteParams p) {
   constexpr int kLanes = D / 8;                  // threads of a row: 16 bytes of bf16 each
   constexpr int kAtOnce = kThreads / kLanes;     // rows in flight
   constexpr int kPasses = kBlk / kAtOnce;
   __shared__ float s_max[kThreads / 32];
+  __shared__ int s_first, s_end, s_old, s_new;   // the request: its tokens, its lengths
   const int tid = threadIdx.x, x = blockIdx.x, head = blockIdx.y;
   const bool values = blockIdx.z != 0;
-  // Request r may touch the work items from cu[r] / 64 + 2r on: one more block
-  // than its tokens fill at either end.
+  // Request r may touch the work items from cu[r] / 64 + 2r on: one more block than its
+  // tokens fill at either end.  The owner is the last that starts at or before this
+  // item; the thread that tests a request has its lengths ready for the others.
   int r = -1;
   for (int i0 = 0; i0 < p.batch; i0 += kThreads) {
-    const int i = i0 + tid;
-    const bool before = i < p.batch && (int64_t)(max(p.cu[min(i, p.batch)], 0) / kBlk) + 2 * (int64_t)i <= x;
+    const int i = min(i0 + tid, p.batch - 1);
+    const int a = p.cu[i], b = p.cu[i + 1], old = p.seqlens[i], now = p.new_seqlens[i];
+    const bool before = i0 + tid < p.batch && (int64_t)(max(a, 0) / kBlk) + 2 * (int64_t)i <= x;
     const int c = __syncthreads_count(before);
+    if (tid == c - 1) s_first = a, s_end = b, s_old = old, s_new = now;
     r += c;
     if (c < kThreads) break;
   }
   if (r < 0) return;
-  const int q0 = p.cu[r], q1 = p.cu[r + 1], old = p.seqlens[r];
+  __syncthreads();
+  const int q0 = s_first, q1 = s_end, old = s_old;
   if (q0 < 0 || q1 < q0 || q1 > p.total || old < 0) {
     if (tid == 0) report_status(p.status, kStatusBadSchedule);
     return;
@@ -97,50 +103,44 @@ __global__ void __launch_bounds__(kThreads) quantize_kv_blocks_kernel(const __gr
   const int n = q1 - q0;
   const int64_t item = x - (int64_t)(q0 / kBlk) - 2 * (int64_t)r;
   // a request that was not granted its blocks keeps its length: nothing to write
-  if (n == 0 || item < 0 || (int64_t)p.new_seqlens[r] - old != n) return;
+  if (n == 0 || item < 0 || (int64_t)s_new - old != n) return;
   const int64_t blk = old / kBlk + item;
   if (blk > ((int64_t)old + n - 1) / kBlk) return;
+  const int row0 = (int)max((int64_t)old - blk * kBlk, (int64_t)0);            // first row written
+  const int64_t t0 = blk * kBlk + row0 - old;                                 // its new token
+  const int rows = (int)min((int64_t)kBlk - row0, n - t0);
+  const int64_t stride = values ? p.v_token_stride : p.k_token_stride;
+  const int sub = tid / kLanes, col = tid % kLanes;
+  const __nv_bfloat16* src =
+      (values ? p.v : p.k) + (q0 + t0 + sub) * stride + head * (values ? p.v_head_stride : p.k_head_stride) + 8 * col;
+  uint4 w[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (sub + i * kAtOnce < rows) w[i] = __ldg(reinterpret_cast<const uint4*>(src + i * kAtOnce * stride));
+  }
+  // the tokens are on their way; where they go
   const int page = blk < p.max_blocks ? p.block_table[(int64_t)r * p.max_blocks + blk] : -1;
   if (page < 0 || page >= p.num_blocks) {
     if (tid == 0) report_status(p.status, kStatusBadBlockTable);
     return;
   }
-  const int row0 = (int)max((int64_t)old - blk * kBlk, (int64_t)0);            // first row written
-  const int64_t t0 = blk * kBlk + row0 - old;                                 // its new token
-  const int rows = (int)min((int64_t)kBlk - row0, n - t0);
-  const __nv_bfloat16* src = (values ? p.v : p.k) + (q0 + t0) * (values ? p.v_token_stride : p.k_token_stride) +
-                             head * (values ? p.v_head_stride : p.k_head_stride);
-  const int64_t stride = values ? p.v_token_stride : p.k_token_stride;
   uint8_t* dst = (values ? p.v_cache + page * p.v_block_bytes : p.k_cache + page * p.k_block_bytes) +
                  (int64_t)head * kBlk * D;
   float* scale = (values ? p.v_scale + page * p.v_scale_stride : p.k_scale + page * p.k_scale_stride) + head;
   const float was = row0 > 0 ? *scale : 0.f;
 
-  const int sub = tid / kLanes, col = tid % kLanes;
-  uint4 w[kPasses];
+  auto lo_of = [](uint32_t b) { return __uint_as_float(b << 16); };
+  auto hi_of = [](uint32_t b) { return __uint_as_float(b & 0xFFFF0000u); };
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    w[i] = make_uint4(0, 0, 0, 0);
-    const int row = sub + i * kAtOnce;
-    if (row < rows) w[i] = __ldg(reinterpret_cast<const uint4*>(src + row * stride + 8 * col));
-  }
-  auto values_of = [](const uint4& u, float (&f)[8]) {
-    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t b[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(v[j] << 16);
-      f[2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    float f[8];
-    values_of(w[i], f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(f[j]);
-      if (a < INFINITY) amax = fmaxf(amax, a);
+      const float u = fabsf(lo_of(b[j])), v = fabsf(hi_of(b[j]));
+      if (u < INFINITY) amax = fmaxf(amax, u);
+      if (v < INFINITY) amax = fmaxf(amax, v);
     }
   }
 #pragma unroll
@@ -153,36 +153,34 @@ __global__ void __launch_bounds__(kThreads) quantize_kv_blocks_kernel(const __gr
   // older tokens of a block whose scale grew
   if (was < now) {
     const float ratio = was / now;
-    for (int i = tid; i < row0 * (D / 16); i += kThreads) {
-      uint4 u = reinterpret_cast<uint4*>(dst)[i];
-      uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float f[4];
-        decode4<kInt8>(v[j], f);
-        v[j] = code4<kInt8>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
-      }
-      reinterpret_cast<uint4*>(dst)[i] = make_uint4(v[0], v[1], v[2], v[3]);
+#pragma unroll 1
+    for (int i = tid; i < row0 * (D / 4); i += kThreads) {
+      float f[4];
+      decode4<kInt8>(reinterpret_cast<uint32_t*>(dst)[i], f);
+      reinterpret_cast<uint32_t*>(dst)[i] = code4<kInt8>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
     }
   }
-  // A power of two divides exactly by its inverse; any other older scale is divided by.
-  const bool pow2 = (__float_as_uint(now) & 0x007FFFFFu) == 0u && now >= 1.17549435e-38f && now < 1.7e38f;
-  const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(now)) : 0.f;
+  uint2* out = reinterpret_cast<uint2*>(dst + (row0 + sub) * D + 8 * col);
+  if ((__float_as_uint(now) & 0x007FFFFFu) == 0u && now < 1.7e38f) {
+    // a power of two (or 0) divides exactly by its inverse
+    const float inv = now > 0.f ? __uint_as_float((254u << 23) - __float_as_uint(now)) : 0.f;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = sub + i * kAtOnce;
-    if (row < rows) {
-      float f[8];
-      values_of(w[i], f);
-      uint2 out = make_uint2(0, 0);
-      if (now > 0.f) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = pow2 ? f[j] * inv : __fdiv_rn(f[j], now);
-        out.x = code4<kInt8>(f[0], f[1], f[2], f[3]);
-        out.y = code4<kInt8>(f[4], f[5], f[6], f[7]);
-      }
-      *reinterpret_cast<uint2*>(dst + (row0 + row) * D + 8 * col) = out;
+    for (int i = 0; i < kPasses; ++i) {
+      // all zeros, infinities beside zeros among them, for a zero scale
+      const uint4 b = now > 0.f ? w[i] : make_uint4(0, 0, 0, 0);
+      const uint2 c = make_uint2(code4<kInt8>(lo_of(b.x) * inv, hi_of(b.x) * inv, lo_of(b.y) * inv, hi_of(b.y) * inv),
+                                 code4<kInt8>(lo_of(b.z) * inv, hi_of(b.z) * inv, lo_of(b.w) * inv, hi_of(b.w) * inv));
+      if (sub + i * kAtOnce < rows) out[i * kAtOnce * (D / 8)] = c;
     }
+  } else {
+    // an older scale of some other kind: divide, reading the tokens again
+#pragma unroll 1
+    for (int i = sub; i < rows; i += kAtOnce)
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) {
+        const float v = __fdiv_rn(__bfloat162float(src[(i - sub) * stride + j]), now);
+        reinterpret_cast<uint8_t*>(out + (i - sub) * (D / 8))[j] = (uint8_t)code4<kInt8>(v, v, v, v);
+      }
   }
   if (tid == 0) *scale = now;
 }
