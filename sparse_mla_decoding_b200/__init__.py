@@ -492,20 +492,26 @@ def quantize_kv(latent: torch.Tensor, rope: torch.Tensor, kvcache: torch.Tensor,
 _paged_words: dict = {}
 
 
-def _paged_word(dev: torch.device) -> Optional[torch.Tensor]:
+def _paged_word(index: int) -> Optional[torch.Tensor]:
     """The status word that the paged calls on a device share when they get no workspace.
 
     Made by the first such call; a graph captured before that reports nowhere
     (an allocation inside the capture would belong to the graph)."""
-    w = _paged_words.get(dev.index)
-    if w is None and not torch.cuda.is_current_stream_capturing():
+    w = _paged_words.get(index)
+    if w is None and not _capturing(index):
         with _ws_lock:
-            w = _paged_words.get(dev.index)
+            w = _paged_words.get(index)
             if w is None:
+                dev = torch.device("cuda", index)
                 w = torch.zeros(64, dtype=torch.int32, device=dev)
                 torch.cuda.current_stream(dev).synchronize()    # other streams may use it next
-                _paged_words[dev.index] = w
+                _paged_words[index] = w
     return w
+
+
+def _capturing(index: int) -> bool:
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def _paged_key(device: Optional[torch.device]) -> int:
@@ -548,20 +554,16 @@ def _block_table(t: torch.Tensor, index: int) -> Tuple[int, int]:
     return t.shape
 
 
-class _OnDevice:
-    """Makes a device current for a launch, if another one is."""
-
-    def __init__(self, index: int):
-        self.index = index
-
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back != self.index:
-            torch.cuda.set_device(self.back)
+def _on_device(index: int, call, *args) -> int:
+    """call(*args) with device `index` current."""
+    back = torch.cuda.current_device()
+    if back == index:
+        return call(*args)
+    torch.cuda.set_device(index)
+    try:
+        return call(*args)
+    finally:
+        torch.cuda.set_device(back)
 
 
 def extend_block_table(block_table: torch.Tensor, cache_seqlens: torch.Tensor, new_lens: torch.Tensor,
@@ -593,17 +595,13 @@ def extend_block_table(block_table: torch.Tensor, cache_seqlens: torch.Tensor, n
     n = int(max_new_tokens)
     if not 0 <= n < 1 << 31:
         _bad("max_new_tokens must be in [0, 2^31)")
-    dev = block_table.device
-    slots = torch.empty(n, dtype=torch.int64, device=dev)
-    cu_new = torch.empty(b + 1, dtype=torch.int32, device=dev)
-    lens = torch.empty(b, dtype=torch.int32, device=dev)
-    left = torch.empty(1, dtype=torch.int32, device=dev)
-    with _OnDevice(index):
-        rc = lib().smla_extend_block_table(block_table.data_ptr(), cols, cache_seqlens.data_ptr(),
-                                           new_lens.data_ptr(), b, free_blocks.data_ptr(), capacity,
-                                           num_free.data_ptr(), n, slots.data_ptr(), cu_new.data_ptr(),
-                                           lens.data_ptr(), left.data_ptr(), _raw_stream(index))
-    _check(rc, "smla_extend_block_table")
+    slots = block_table.new_empty(n, dtype=torch.int64)
+    cu_new, lens, left = block_table.new_empty(b + 1), block_table.new_empty(b), block_table.new_empty(1)
+    rc = _on_device(index, lib().smla_extend_block_table, block_table.data_ptr(), cols, cache_seqlens.data_ptr(),
+                    new_lens.data_ptr(), b, free_blocks.data_ptr(), capacity, num_free.data_ptr(), n,
+                    slots.data_ptr(), cu_new.data_ptr(), lens.data_ptr(), left.data_ptr(), _raw_stream(index))
+    if rc:
+        _check(rc, "smla_extend_block_table")
     return slots, cu_new, lens, left
 
 
@@ -616,22 +614,21 @@ def _q8_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tenso
     if fmt is None or len(shape) != 4 or index < 0 or shape[2] != BLOCK_SIZE or shape[3] not in (64, 128):
         _bad("k_cache must be e4m3 or int8 [num_blocks, h_kv, 64, 64 or 128] on CUDA")
     nb, h_kv, _, d = shape
-    block = h_kv * BLOCK_SIZE * d
-    strides = []
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != k_cache.dtype or t.shape != shape or t.get_device() != index:
-            _bad(f"{name} must match k_cache's type, shape and device")
-        st = t.stride()
-        if (h_kv > 1 and st[1] != BLOCK_SIZE * d) or st[2] != d or st[3] != 1:
-            _bad(f"{name} must be dense within a block")
-        strides.append(st[0] if nb > 1 else block)      # a lone block's stride is free to say anything
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        st = t.stride()
-        if t.dtype != torch.float32 or t.shape != (nb, h_kv) or t.get_device() != index or (h_kv > 1 and st[1] != 1):
+    ks, vs, kss, vss = k_cache.stride(), v_cache.stride(), k_scale.stride(), v_scale.stride()
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != shape or v_cache.get_device() != index:
+        _bad("v_cache must match k_cache's type, shape and device")
+    inside = (BLOCK_SIZE * d, d, 1)
+    if (ks[1:] != inside or vs[1:] != inside) and (h_kv > 1 or ks[2:] != inside[1:] or vs[2:] != inside[1:]):
+        _bad("k_cache and v_cache must be dense within a block")
+    rows = (nb, h_kv)
+    for name, t, st in (("k_scale", k_scale, kss), ("v_scale", v_scale, vss)):
+        if t.dtype != torch.float32 or t.shape != rows or t.get_device() != index or (st[1] != 1 and h_kv > 1):
             _bad(f"{name} must be float32 [num_blocks, h_kv] on cuda:{index}")
-        strides.append(st[0] if nb > 1 else h_kv)
-    return _Q8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, *strides, h_kv,
-                    d, fmt)
+    if nb == 1:                      # a lone block's stride is free to say anything
+        ks = vs = (h_kv * BLOCK_SIZE * d,)
+        kss = vss = (h_kv,)
+    return _Q8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, ks[0], vs[0],
+                    kss[0], vss[0], h_kv, d, fmt)
 
 
 def _rows16(t: torch.Tensor) -> torch.Tensor:
@@ -670,13 +667,12 @@ def quantize_kv_blocks(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, 
     cu_new = _i32_vector(cu_new, b + 1, "cu_new", index)
     k, v = _rows16(k), _rows16(v)
     ks, vs = k.stride(), v.stride()
-    with _OnDevice(index):
-        word = _paged_word(k_cache.device)
-        rc = lib().smla_quantize_kv_blocks(k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1], shape[0],
-                                           ctypes.byref(cache), block_table.data_ptr(), cols, b,
-                                           cache_seqlens.data_ptr(), new_seqlens.data_ptr(), cu_new.data_ptr(),
-                                           _ptr(word), _raw_stream(index))
-    _check(rc, "smla_quantize_kv_blocks")
+    word = _paged_word(index)
+    rc = _on_device(index, lib().smla_quantize_kv_blocks, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
+                    shape[0], ctypes.byref(cache), block_table.data_ptr(), cols, b, cache_seqlens.data_ptr(),
+                    new_seqlens.data_ptr(), cu_new.data_ptr(), _ptr(word), _raw_stream(index))
+    if rc:
+        _check(rc, "smla_quantize_kv_blocks")
     if check_device_status and word is not None:
         _raise_on_flags(word, "smla_quantize_kv_blocks")
 
@@ -769,33 +765,32 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         scale = float(softmax_scale)
         if not 0.0 < scale < math.inf:
             _bad("softmax_scale must be > 0 and finite")
-    dev = k_cache.device
     if out is None:
-        o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+        o, lse = q.new_empty(shape), k_scale.new_empty(shape[:-1])
     else:
         o, lse = out
         for name, t, dt, sh in (("o", o, torch.bfloat16, shape), ("lse", lse, torch.float32, shape[:-1])):
             if t.dtype != dt or t.shape != sh or t.get_device() != index or not t.is_contiguous():
-                _bad(f"out: {name} must be contiguous {dt} {list(sh)} on {dev}")
-        o = o if o.data_ptr() % 16 == 0 else _bad("out: o must be 16-byte aligned")
-    with _OnDevice(index):
-        L = lib()
-        nbytes = L.smla_gqa_workspace_bytes(d, index)
-        if workspace is None:
-            word, scratch = _paged_word(dev), torch.empty(nbytes, dtype=torch.uint8, device=dev)
-            at, room = scratch.data_ptr(), nbytes
-        else:
-            if (workspace.get_device() != index or not workspace.is_contiguous() or workspace.dtype != torch.uint8 or
-                    workspace.numel() < 256 + nbytes):
-                _bad(f"workspace needs {256 + nbytes} bytes of uint8 on {dev}")
-            word, at, room = workspace, workspace.data_ptr() + 256, workspace.numel() - 256
-        rc = L.smla_gqa_attention_with_kvcache(
-            q.data_ptr(), q.stride(0), q.stride(1), total, h_q, ctypes.byref(cache), block_table.data_ptr(), cols, b,
-            cache_seqlens.data_ptr(), cu, s_q, total if max_seqlen_q is None else int(max_seqlen_q),
-            1 if causal else 0, scale, softcap, _ptr(alibi_slopes), _ptr(prefix_lens), _ptr(doc_bounds),
-            o.data_ptr(), lse.data_ptr(), at, room, _ptr(word), _raw_stream(index))
-    _check(rc, "smla_gqa_attention_with_kvcache")
+                _bad(f"out: {name} must be contiguous {dt} {list(sh)} on cuda:{index}")
+        if o.data_ptr() % 16:
+            _bad("out: o must be 16-byte aligned")
+    L = lib()
+    nbytes = L.smla_gqa_workspace_bytes(d, index)
+    if workspace is None:
+        word, scratch = _paged_word(index), k_scale.new_empty(nbytes // 4)
+        at, room = scratch.data_ptr(), nbytes
+    else:
+        if (workspace.get_device() != index or not workspace.is_contiguous() or workspace.dtype != torch.uint8 or
+                workspace.numel() < 256 + nbytes):
+            _bad(f"workspace needs {256 + nbytes} bytes of uint8 on cuda:{index}")
+        word, at, room = workspace, workspace.data_ptr() + 256, workspace.numel() - 256
+    rc = _on_device(
+        index, L.smla_gqa_attention_with_kvcache, q.data_ptr(), q.stride(0), q.stride(1), total, h_q,
+        ctypes.byref(cache), block_table.data_ptr(), cols, b, cache_seqlens.data_ptr(), cu, s_q,
+        total if max_seqlen_q is None else int(max_seqlen_q), 1 if causal else 0, scale, softcap, _ptr(alibi_slopes),
+        _ptr(prefix_lens), _ptr(doc_bounds), o.data_ptr(), lse.data_ptr(), at, room, _ptr(word), _raw_stream(index))
+    if rc:
+        _check(rc, "smla_gqa_attention_with_kvcache")
     if check_device_status and word is not None:
         _raise_on_flags(word, "smla_gqa_attention_with_kvcache")
     return o, lse

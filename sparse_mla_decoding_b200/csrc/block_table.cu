@@ -135,7 +135,8 @@ extern "C" int smla_extend_block_table(int32_t* block_table, int max_blocks, con
                                        int64_t free_capacity, const int32_t* num_free, int64_t max_new_tokens,
                                        int64_t* slot_mapping, int32_t* cu_new, int32_t* seqlens_out,
                                        int32_t* num_free_out, void* stream) {
-  if (batch < 0 || max_blocks < 1 || free_capacity < 0 || free_capacity > 0x7FFFFFFF || max_new_tokens < 0 || max_new_tokens > 0x7FFFFFFF)
+  if (batch < 0 || max_blocks < 1 || free_capacity < 0 || free_capacity > 0x7FFFFFFF || max_new_tokens < 0 ||
+      max_new_tokens > 0x7FFFFFFF)
     return SMLA_ERR_INVALID_ARGUMENT;
   if (!num_free || !cu_new || !num_free_out || (max_new_tokens > 0 && !slot_mapping) ||
       (free_capacity > 0 && !free_blocks))

@@ -112,6 +112,21 @@ Layout workspace(int head_dim, int ctas) {
 
 }  // namespace
 
+namespace smla {
+
+cudaError_t raise_shared_limit(SharedLimit& done, const void* kernel, int bytes) {
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  void* ctx = current_context();
+  std::atomic<void*>& known = done.done[dev & 63];
+  if (dev < 64 && ctx != nullptr && known.load(std::memory_order_acquire) == ctx) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) known.store(ctx != nullptr ? ctx : current_context(), std::memory_order_release);
+  return e;
+}
+
+}  // namespace smla
+
 extern "C" {
 
 int smla_quantize_kv_blocks(const void* k, const void* v, int64_t k_token_stride, int64_t k_head_stride,

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "q8_cache.h"
@@ -34,5 +35,12 @@ cudaError_t launch_q8_decode(const Q8Params& p, bool int8, int rows, const CUten
 
 // The tensor-core kernel for many new tokens: no scratch, one CTA per 256 rows.
 cudaError_t launch_q8_prefill(const Q8Params& p, bool int8, cudaStream_t stream);
+
+// Raises a kernel's shared memory limit, once per device context (`done`, one per
+// kernel, remembers the contexts; after a device reset the context is a new one).
+struct SharedLimit {
+  std::atomic<void*> done[64];
+};
+cudaError_t raise_shared_limit(SharedLimit& done, const void* kernel, int bytes);
 
 }  // namespace smla

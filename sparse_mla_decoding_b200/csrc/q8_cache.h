@@ -171,17 +171,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// x_j = cap tanh(x_j fc) of N scores; one vote of the warp for the N picks the way.
-// All |x| <= 0.75: x P(x^2), P a degree-5 fit to tanh(x)/x in relative error (1.6e-7
-// in fp32; reweighted least squares on Chebyshev nodes), so small scores keep their
-// relative precision and no special function is used.  Else 1 - 2 / (1 + exp(2 |x|))
-// with the sign of x, off by some 1e-7 of the cap.
+// x_j = cap tanh(x_j fc) of N scores; a vote of the warp over the N picks the way.
+// All |y| = |x fc| <= 0.35: y P(y^2), P a degree-3 fit to tanh(y)/y in relative error
+// (reweighted least squares on Chebyshev nodes; 1.5e-7 in fp32), so small scores keep
+// their relative precision and no special function is used; fc and cap go into the
+// coefficients, so a score costs 2.5 packed instructions.  Else 1 - 2 / (1 + exp(2
+// |y|)) with the sign of x, off by some 1e-7 of the cap.  (x is a product of f16
+// values, below 2^18, so x^2 stays in range.)
 template <int N>
 __device__ __forceinline__ void cap_scores(float* x, float fc, float cap) {
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < N; j += 2) top = max3(top, fabsf(x[j]), fabsf(x[j + 1]));
-  if (__any_sync(0xffffffffu, !(top * fc <= 0.75f))) {
+  if (__any_sync(0xffffffffu, !(top * fc <= 0.35f))) {
     const float fe = fc * (2.f * kLog2e);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -190,14 +192,13 @@ __device__ __forceinline__ void cap_scores(float* x, float fc, float cap) {
       x[j] = copysignf(fmaf(-2.f * cap, r, cap), x[j]);
     }
   } else {
+    const float s = fc * fc, c0 = fc * cap, c1 = c0 * s, c2 = c1 * s;
+    const float2 k0 = both(c0 * 0.9999999403953552f), k1 = both(c1 * -0.33332422375679016f),
+                 k2 = both(c2 * 0.13295817375183105f), k3 = both(c2 * s * -0.04895907640457153f);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
-      const float2 y = mul2(make_float2(x[j], x[j + 1]), both(fc)), z = mul2(y, y);
-      float2 r = fma2(both(-0.004716585855931044f), z, both(0.01958341710269451f));
-      r = fma2(r, z, both(-0.0533447191119194f));
-      r = fma2(r, z, both(0.13325412571430206f));
-      r = fma2(r, z, both(-0.33332958817481995f));
-      r = mul2(fma2(r, z, both(1.0f)), mul2(y, both(cap)));
+      const float2 v = make_float2(x[j], x[j + 1]), z = mul2(v, v);
+      const float2 r = mul2(fma2(fma2(fma2(k3, z, k2), z, k1), z, k0), v);
       x[j] = r.x;
       x[j + 1] = r.y;
     }

@@ -524,8 +524,9 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
 #pragma unroll
         for (int k = 0; k < kPer / 8; ++k) raw_q[nt][k] = make_uint4(0, 0, 0, 0);
         if (t < x.n) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(x.q0 + t) * p.q_token_stride +
-                                                            (int64_t)(head * p.group + hh) * p.q_head_stride + kPer * c);
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + (int64_t)(x.q0 + t) * p.q_token_stride + (int64_t)(head * p.group + hh) * p.q_head_stride +
+              kPer * c);
 #pragma unroll
           for (int k = 0; k < kPer / 8; ++k) raw_q[nt][k] = __ldg(src + k);
         }
@@ -762,7 +763,8 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
       if (++slot == kSlots) slot = 0, phase ^= 1;
     }
 
-  // ---- merge what the CTA has of each unit, the rows of all units over the warps.  A chain of pieces starts at a tail, or at the head of warp 0.
+  // ---- merge what the CTA has of each unit, the rows of all units over the warps.  A
+  // chain of pieces starts at a tail, or at the head of warp 0.
   __syncthreads();
   int turn = 0;
 #pragma unroll 1
@@ -772,7 +774,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
     if (!start.there) continue;
     const int first = begun ? s : 0;
     int last = first;
-    while (last + 1 < kWarps && (begun && last == first ? true : !sm.head[last].ends) && sm.head[last + 1].there) ++last;
+    while (last + 1 < kWarps && ((begun && last == first) || !sm.head[last].ends) && sm.head[last + 1].there) ++last;
     const bool ended = begun && last == first ? false : sm.head[last].ends != 0;
     const int rows = min(kRows, start.n * p.group - start.rt * kRows);
     const int p0 = blockIdx.x * kWarps + first, p1 = blockIdx.x * kWarps + last;
@@ -848,9 +850,8 @@ template <int D, bool kInt8, int NT>
 cudaError_t launch(const Q8Params& p, const CUtensorMap& k_map, const CUtensorMap& v_map, const Q8Scratch& scratch,
                    int ctas, cudaStream_t stream) {
   constexpr int kWarps = kWarpsOf<D, NT>, kBytes = kSharedBytes<D, NT>;
-  // per call: the attribute belongs to the current context and costs no launch
-  if (const cudaError_t e = cudaFuncSetAttribute(q8_decode_kernel<D, kInt8, NT>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  static SharedLimit limit;
+  if (const cudaError_t e = raise_shared_limit(limit, (const void*)q8_decode_kernel<D, kInt8, NT>, kBytes);
       e != cudaSuccess)
     return e;
   q8_decode_kernel<D, kInt8, NT><<<ctas, kWarps * 32, kBytes, stream>>>(p, k_map, v_map, scratch);

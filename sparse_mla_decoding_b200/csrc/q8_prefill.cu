@@ -70,6 +70,7 @@ struct PrefillShared {                    // at a 1024-byte boundary
   uint8_t k[kStages][kBlk * D * 2];
   uint8_t v[kStages][kBlk * D * 2];
   BlockScales scales[kScaleRing];
+  float2 bias[2 * kTileRows];             // of a row: position, and slope in base 2
   uint64_t full[kStages];                 // K and V of a block
   uint64_t sfull[2][2], pfull[2][2];      // [row tile][block % 2]
   uint64_t odone[2][2], qfull;
@@ -333,12 +334,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     // ================================ softmax ================================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split::kSoftmax));
     // This thread's row: token, query head, and which positions it sees.
-    int lo = 0, hi = 0x7FFFFFFF, t = 0, hq = 0;
+    int lo = 0, hi = 0x7FFFFFFF;
     int64_t q_at = -1;                                // in q; -1: no row
     if (row0 + tid < rows_all) {
-      t = (int)(row0 + tid) / p.group;
-      hq = head * p.group + (int)(row0 + tid) - t * p.group;
+      const int t = (int)(row0 + tid) / p.group, hq = head * p.group + (int)(row0 + tid) - t * p.group;
       q8_visible(p, x, t, lo, hi);
+      if (kMods && p.slopes) sm.bias[tid] = make_float2((float)(x.len - x.n + t), p.slopes[hq] * kLog2e);
       q_at = (int64_t)(x.q0 + t) * p.q_token_stride + (int64_t)hq * p.q_head_stride;
     }
     // Q: each row scaled by a power of two, as f16.  A warp copies the 32 rows of its
@@ -384,8 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       if (lane == 0) mbar_arrive1(&sm.qfull);
     }
     const uint32_t s_addr = tmem + 128 * w + ((uint32_t)(32 * (warp & 3)) << 16), o_addr = s_addr + 256;
-    const float slope = p.slopes ? p.slopes[hq] * kLog2e : 0.f;
-    const float pos = (float)(x.len - x.n + t);
     const float fs = row_fac * p.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -407,12 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         // capped and biased scores in place (f then is 1)
         if constexpr (kMods) {
           if (p.cap > 0.f) {
-            cap_scores<32>(S, fs * bs.k * p.inv_cap_log2, p.cap_log2);
-            cap_scores<32>(S + 32, fs * bs.k * p.inv_cap_log2, p.cap_log2);
+            cap_scores<64>(S, fs * bs.k * p.inv_cap_log2, p.cap_log2);
             f = 1.f;
           }
           if (p.slopes) {
-            const float2 d = make_float2(pos - (float)j0, pos - (float)(j0 + 1));
+            const float2 b = sm.bias[tid];
+            const float slope = b.y;
+            const float2 d = make_float2(b.x - (float)j0, b.x - (float)(j0 + 1));
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
               const float2 y = mul2(make_float2(S[j], S[j + 1]), both(f));
@@ -694,12 +694,14 @@ namespace {
 template <int D, bool kInt8, bool kMods>
 cudaError_t launch_as(const Q8Params& p, cudaStream_t stream) {
   constexpr int kBytes = sizeof(PrefillShared<D>) + 1024;
-  cudaFuncAttributes at;
-  if (const cudaError_t e = cudaFuncGetAttributes(&at, q8_prefill_kernel<D, kInt8, kMods>); e != cudaSuccess) return e;
   // a register split above what the CTA is launched with would wait for ever
-  if (at.numRegs * kThreads < Split::kAll) return cudaErrorInvalidConfiguration;
-  if (const cudaError_t e = cudaFuncSetAttribute(q8_prefill_kernel<D, kInt8, kMods>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  static const int regs = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, q8_prefill_kernel<D, kInt8, kMods>) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs * kThreads < Split::kAll) return cudaErrorInvalidConfiguration;
+  static SharedLimit limit;
+  if (const cudaError_t e = raise_shared_limit(limit, (const void*)q8_prefill_kernel<D, kInt8, kMods>, kBytes);
       e != cudaSuccess)
     return e;
   const int64_t items = (int64_t)p.total_q * p.group / (2 * kTileRows) + p.batch;
