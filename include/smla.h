@@ -344,7 +344,7 @@ int smla_flash_mla_with_kvcache_static_scratch(const void* q, const uint8_t* kvc
  *                      of one request and head within 2^60 of one another
  *   *_block_stride   : bytes between blocks, a multiple of 16
  *   *_scale_stride   : floats between the scales of neighbouring blocks
- *   head_dim         : 64 or 128;  h_kv * head_dim * 64 < 2^31
+ *   head_dim         : 64 or 128;  h_kv at most 65535, h_kv * head_dim * 64 < 2^31
  *   format           : SMLA_Q8_E4M3 or SMLA_Q8_INT8
  */
 typedef struct {
@@ -415,8 +415,10 @@ int smla_extend_block_table(int32_t* block_table, int max_blocks, const int32_t*
  *   cu_new        : device int32 [batch + 1]
  *   status        : device uint32, sticky flags as in a workspace's status word
  *                   (see smla_get_device_status), or NULL: a block outside the
- *                   table or the cache is skipped and flagged, token offsets
- *                   that are not increasing within total_new likewise
+ *                   table or the cache is skipped and flagged, and so is a
+ *                   request whose token offsets run backwards or past
+ *                   total_new (other requests of such a call may be skipped
+ *                   with it)
  */
 int smla_quantize_kv_blocks(const void* k, const void* v, int64_t k_token_stride, int64_t k_head_stride,
                             int64_t v_token_stride, int64_t v_head_stride, int64_t total_new,
@@ -460,12 +462,13 @@ size_t smla_gqa_workspace_bytes(int head_dim, int device);
  *   workspace    : device, >= smla_gqa_workspace_bytes, 256-byte aligned; calls
  *                  that may run at the same time need workspaces of their own
  *   status       : as for smla_quantize_kv_blocks
- * h_q is a multiple of h_kv, below 2^20; total_q * h_q < 2^31.  Rows of q that belong to no
- * request are not read and their outputs not written.  A position whose block
- * lies outside the table or the cache is skipped and flagged.  What the cache
- * holds behind a request's length never reaches a result; a NaN in a value row
- * within it reaches every token of the request that shares a tile with one
- * that sees it.
+ * h_q is a multiple of h_kv, below 2^20; total_q * h_q < 2^31.  Rows of q that
+ * belong to no request are not read and their outputs not written.  A position
+ * whose block lies outside the table or the cache is skipped and flagged; so is
+ * a request whose token offsets run backwards or past total_q (other requests
+ * of such a call may be skipped with it).  What the cache holds behind a
+ * request's length never reaches a result; a NaN in a value row within it
+ * reaches every token of the request that shares a tile with one that sees it.
  */
 int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t total_q,
                                     int h_q, const smla_q8_cache* cache, const int32_t* block_table, int max_blocks,

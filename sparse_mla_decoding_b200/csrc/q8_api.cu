@@ -24,7 +24,7 @@ int check_cache(const smla_q8_cache* c) {
   if (!c) return SMLA_ERR_INVALID_ARGUMENT;
   if (c->head_dim != 64 && c->head_dim != 128) return SMLA_ERR_UNSUPPORTED;
   if (c->format != SMLA_Q8_E4M3 && c->format != SMLA_Q8_INT8) return SMLA_ERR_UNSUPPORTED;
-  if (c->h_kv < 1 || (int64_t)c->h_kv * c->head_dim * smla::kBlk > 0x7FFFFFFF) return SMLA_ERR_INVALID_ARGUMENT;
+  if (c->h_kv < 1 || c->h_kv > 65535 || (int64_t)c->h_kv * c->head_dim * smla::kBlk > 0x7FFFFFFF) return SMLA_ERR_INVALID_ARGUMENT;
   if (!c->k_cache || !c->v_cache || !c->k_scale || !c->v_scale) return SMLA_ERR_INVALID_ARGUMENT;
   const int64_t dense = (int64_t)c->h_kv * c->head_dim * smla::kBlk;
   if (c->num_blocks < 1 || c->num_blocks > 0x7FFFFFFF / smla::kBlk) return SMLA_ERR_INVALID_ARGUMENT;
@@ -135,8 +135,7 @@ int smla_quantize_kv_blocks(const void* k, const void* v, int64_t k_token_stride
                             const int32_t* cache_seqlens, const int32_t* new_seqlens, const int32_t* cu_new,
                             uint32_t* status, void* stream) {
   if (int rc = check_cache(cache)) return rc;
-  if (batch < 0 || max_blocks < 1 || total_new < 0 || total_new > 0x7FFFFFFF || batch > (1 << 28) ||
-      cache->h_kv > 65535)
+  if (batch < 0 || max_blocks < 1 || total_new < 0 || total_new > 0x7FFFFFFF || batch > (1 << 28))
     return SMLA_ERR_INVALID_ARGUMENT;
   if (batch == 0 || total_new == 0) return SMLA_OK;
   if (!k || !v || !block_table || !cache_seqlens || !new_seqlens || !cu_new) return SMLA_ERR_INVALID_ARGUMENT;

@@ -259,24 +259,22 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     Q8Request mine{0, 0, 0, 0};
     if (i < p.batch) {
       mine = q8_request(p, i, &bad);
+      if (bad && blockIdx.x + blockIdx.y == 0) report_status(p.status, kStatusBadSchedule);
       const int64_t c = p.cu_q ? max(p.cu_q[i], 0) : (int64_t)i * p.s_q;
       before = c * p.group / (2 * kTileRows) + i <= item;
     }
     const int c = __syncthreads_count(before);
-    if (tid == c - 1) {
+    if (c > 0 && r == i0 - 1 && tid == c - 1) {
       sm.x = mine;
       sm.bad = bad;
     }
-    r += c;
-    if (c < kThreads) break;
+    if (r == i0 - 1) r += c;
+    if (c < kThreads && blockIdx.x + blockIdx.y > 0) break;   // the first CTA looks them all over
   }
   if (r < 0) return;
   __syncthreads();
   const Q8Request x = sm.x;
-  if (sm.bad) {
-    if (tid == 0) report_status(p.status, kStatusBadSchedule);
-    return;
-  }
+  if (sm.bad) return;
   const int64_t tile = item - ((int64_t)x.q0 * p.group / (2 * kTileRows) + r);
   const int64_t rows_all = (int64_t)x.n * p.group, row0 = tile * 2 * kTileRows;
   if (tile < 0 || row0 >= rows_all) return;

@@ -87,19 +87,18 @@ __global__ void __launch_bounds__(kThreads, 8) quantize_kv_blocks_kernel(const _
   for (int i0 = 0; i0 < p.batch; i0 += kThreads) {
     const int i = min(i0 + tid, p.batch - 1);
     const int a = p.cu[i], b = p.cu[i + 1], old = p.seqlens[i], now = p.new_seqlens[i];
+    if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && (a < 0 || b < a || b > p.total || old < 0))
+      report_status(p.status, kStatusBadSchedule);
     const bool before = i0 + tid < p.batch && (int64_t)(max(a, 0) / kBlk) + 2 * (int64_t)i <= x;
     const int c = __syncthreads_count(before);
-    if (tid == c - 1) s_first = a, s_end = b, s_old = old, s_new = now;
-    r += c;
-    if (c < kThreads) break;
+    if (c > 0 && r == i0 - 1 && tid == c - 1) s_first = a, s_end = b, s_old = old, s_new = now;
+    if (r == i0 - 1) r += c;
+    if (c < kThreads && blockIdx.x + blockIdx.y + blockIdx.z > 0) break;   // the first CTA looks them all over
   }
   if (r < 0) return;
   __syncthreads();
   const int q0 = s_first, q1 = s_end, old = s_old;
-  if (q0 < 0 || q1 < q0 || q1 > p.total || old < 0) {
-    if (tid == 0) report_status(p.status, kStatusBadSchedule);
-    return;
-  }
+  if (q0 < 0 || q1 < q0 || q1 > p.total || old < 0) return;
   const int n = q1 - q0;
   const int64_t item = x - (int64_t)(q0 / kBlk) - 2 * (int64_t)r;
   // a request that was not granted its blocks keeps its length: nothing to write

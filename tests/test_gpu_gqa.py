@@ -245,6 +245,46 @@ def test_bad_offsets_are_flagged_and_leave_the_others():
     U.compare(o[:1], lse[:1], [a[:1] for a in ref])
 
 
+def test_bad_offsets_of_long_requests_are_flagged():
+    """More than the decode kernel's rows: the request that runs past the end is left out."""
+    x = build([40, 50], [100, 80], 4, 2, 64, "e4m3", 1320)
+    ref = reference(x)
+    x["cu"] = np.array([0, 40, 91], np.int32)
+    o, lse, (status, raw) = call(x)
+    assert status == 1 and raw & 4
+    U.compare(o[:40], lse[:40], [a[:40] for a in ref])
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_blocks_past_two_gigabytes(n):
+    """A cache of more than 2^31 bytes a side, with the request's blocks at its end."""
+    import sparse_mla_decoding_b200 as smla
+    x = build([n], [200], 16, 8, 128, "int8", 1350, poison=False)
+    nb, used = 33000, x["kc"].shape[0]
+    big = {}
+    for c, s in (("kc", "ks"), ("vc", "vs")):
+        big[c] = torch.empty(nb, 8, 64, 128, dtype=torch.int8, device="cuda")
+        big[s] = torch.empty(nb, 8, device="cuda")
+        big[c][nb - used:] = x[c].cuda()
+        big[s][nb - used:] = x[s].cuda()
+    table = torch.from_numpy(x["table"]).cuda()
+    table[:, :4] += nb - used
+    args = [torch.from_numpy(x[k]).cuda() for k in ("lens", "cu")]
+    o, lse = smla.gqa_attention_with_kvcache(x["q"].cuda(), big["kc"], big["vc"], big["ks"], big["vs"], table, args[0],
+                                             cu_seqlens_q=args[1], check_device_status=True)
+    U.compare(o, lse, reference(x))
+    k = torch.randn(3, 8, 128, device="cuda").to(torch.bfloat16)
+    cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    before = big["kc"][nb - used:].clone()
+    smla.quantize_kv_blocks(k, k, big["kc"], big["vc"], big["ks"], big["vs"], table, args[0] - 3, args[0], cu,
+                            check_device_status=True)
+    last = int(table[0, 3])
+    rows = big["kc"][last, :, 5:8].float() * big["ks"][last][:, None, None]
+    assert (rows - k.float().transpose(0, 1)).abs().max() <= big["ks"][last].max() / 2
+    before[last - (nb - used)] = big["kc"][last]
+    assert torch.equal(before, big["kc"][nb - used:])
+
+
 def test_repeated_calls_are_bitwise_equal():
     x = build([1, 2, 30], [5000, 900, 300], 16, 2, 128, "e4m3", 1400)
     first = call(x)
