@@ -451,10 +451,13 @@ size_t smla_gqa_workspace_bytes(int head_dim, int device);
  *   q            : device bf16 [total_q][h_q][head_dim] with the given strides
  *                  (elements, multiples of 8), 16-byte aligned
  *   cache        : host struct; read
- *   max_seqlen_q : host hint, the most query tokens of a request; it picks the
- *                  kernel and does not change what is computed
- *   softmax_scale: <= 0 or NaN selects 1/sqrt(head_dim);  softcap: 0 = none
- *   alibi_slopes : device float32 [h_q] or NULL
+ *   max_seqlen_q : host hint, the most query tokens of a request; with total_q,
+ *                  batch and the heads it picks the kernel and does not change
+ *                  what is computed (above total_q: the one for long prompts)
+ *   softmax_scale: <= 0 or NaN selects 1/sqrt(head_dim), else a normal number
+ *   softcap      : 0 = none, else 2^-60 .. 2^60
+ *   alibi_slopes : device float32 [h_q] or NULL; distances are taken in fp32,
+ *                  exact below 2^24 positions
  *   prefix_lens  : device int32 [batch] or NULL (needs causal)
  *   doc_bounds   : device int32 [total_q][2] or NULL, 8-byte aligned
  *   o            : device bf16 [total_q][h_q][head_dim], dense, 16-byte aligned

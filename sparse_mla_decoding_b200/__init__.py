@@ -707,7 +707,7 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     request's query tokens are its last positions and are already in the cache, so
     cache_seqlens (int32 [b]) counts them.  One new token per request, several, or whole
     prompts: max_seqlen_q (the most query tokens of a request; total_q if not given) only
-    picks the kernel.
+    helps to pick the kernel (above total_q: the one for long prompts).
     Scores are softmax_scale * <q, k> (default 1/sqrt(d)), then softcap * tanh(x / softcap)
     with softcap > 0, then minus alibi_slopes[h] * distance (float32 [h_q]).
     A token at position p sees j <= p (causal), every j < prefix_lens[r] as well (int32
@@ -758,13 +758,13 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         if doc_bounds.data_ptr() % 8:
             doc_bounds = doc_bounds.clone()
     softcap = float(softcap)
-    if not 0.0 <= softcap < math.inf:
-        _bad("softcap must be >= 0 and finite")
+    if softcap != 0.0 and not 2.0 ** -60 <= softcap <= 2.0 ** 60:
+        _bad("softcap must be 0 or from 2^-60 to 2^60")
     scale = -1.0
     if softmax_scale is not None:
         scale = float(softmax_scale)
-        if not 0.0 < scale < math.inf:
-            _bad("softmax_scale must be > 0 and finite")
+        if not 2.0 ** -126 <= scale < 2.0 ** 127:
+            _bad("softmax_scale must be > 0 and finite (as a normal float32)")
     if out is None:
         o, lse = q.new_empty(shape), k_scale.new_empty(shape[:-1])
     else:

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -24,7 +25,8 @@ int check_cache(const smla_q8_cache* c) {
   if (!c) return SMLA_ERR_INVALID_ARGUMENT;
   if (c->head_dim != 64 && c->head_dim != 128) return SMLA_ERR_UNSUPPORTED;
   if (c->format != SMLA_Q8_E4M3 && c->format != SMLA_Q8_INT8) return SMLA_ERR_UNSUPPORTED;
-  if (c->h_kv < 1 || c->h_kv > 65535 || (int64_t)c->h_kv * c->head_dim * smla::kBlk > 0x7FFFFFFF) return SMLA_ERR_INVALID_ARGUMENT;
+  if (c->h_kv < 1 || c->h_kv > 65535 || (int64_t)c->h_kv * c->head_dim * smla::kBlk > 0x7FFFFFFF)
+    return SMLA_ERR_INVALID_ARGUMENT;
   if (!c->k_cache || !c->v_cache || !c->k_scale || !c->v_scale) return SMLA_ERR_INVALID_ARGUMENT;
   const int64_t dense = (int64_t)c->h_kv * c->head_dim * smla::kBlk;
   if (c->num_blocks < 1 || c->num_blocks > 0x7FFFFFFF / smla::kBlk) return SMLA_ERR_INVALID_ARGUMENT;
@@ -38,6 +40,9 @@ int check_cache(const smla_q8_cache* c) {
     return SMLA_ERR_INVALID_ARGUMENT;
   return SMLA_OK;
 }
+
+// A cap whose inverse and whose products with scores stay well inside fp32.
+bool good_cap(float x) { return x >= 0x1p-60f && x <= 0x1p60f; }
 
 bool good_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s <= kMost / 0x10000; }
 
@@ -193,7 +198,8 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
       max_seqlen_q < 0)
     return SMLA_ERR_INVALID_ARGUMENT;
   if (!cu_seqlens_q && (s_q < 0 || (int64_t)batch * s_q != total_q)) return SMLA_ERR_INVALID_ARGUMENT;
-  if (!(softcap >= 0.f) || std::isinf(softcap) || std::isinf(softmax_scale)) return SMLA_ERR_INVALID_ARGUMENT;
+  if (softcap != 0.f && !good_cap(softcap)) return SMLA_ERR_INVALID_ARGUMENT;
+  if (softmax_scale > 0.f && !std::isnormal(softmax_scale)) return SMLA_ERR_INVALID_ARGUMENT;
   if (prefix_lens && !causal) return SMLA_ERR_INVALID_ARGUMENT;
   if (batch == 0 || total_q == 0) return SMLA_OK;
   if (!q || !block_table || !cache_seqlens || !o || !lse || !workspace_ptr) return SMLA_ERR_INVALID_ARGUMENT;
@@ -245,7 +251,7 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   p.lse = lse;
   p.status = status;
   const bool int8 = cache->format == SMLA_Q8_INT8;
-  if ((int64_t)max_seqlen_q * p.group > smla::kQ8DecodeRows) {
+  if (!smla::q8_decode_pays(batch, cache->h_kv, p.group, total_q, max_seqlen_q, doc_bounds != nullptr, sms)) {
     const cudaError_t e = smla::launch_q8_prefill(p, int8, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SMLA_OK : smla::cuda_failure(e);
   }
@@ -253,13 +259,14 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   if (int rc = tile_map(&k_map, cache->k_cache, cache, cache->k_block_stride)) return rc;
   if (int rc = tile_map(&v_map, cache->v_cache, cache, cache->v_block_stride)) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace_ptr);
+  const int rows = (int)std::min<int64_t>(std::min<int64_t>(max_seqlen_q, total_q) * p.group, 0x7FFFFFFF);
   smla::Q8Scratch scratch;
   scratch.o = reinterpret_cast<float*>(ws);
   scratch.cta_o = reinterpret_cast<float*>(ws + wl.cta_o_off);
   scratch.lse = reinterpret_cast<float*>(ws + wl.lse_off);
   scratch.cta_lse = reinterpret_cast<float*>(ws + wl.cta_lse_off);
   scratch.meta = reinterpret_cast<int32_t*>(ws + wl.meta_off);
-  const cudaError_t e = smla::launch_q8_decode(p, int8, max_seqlen_q * p.group, k_map, v_map, scratch, sms,
+  const cudaError_t e = smla::launch_q8_decode(p, int8, rows, k_map, v_map, scratch, sms,
                                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SMLA_OK : smla::cuda_failure(e);
 }

@@ -66,7 +66,7 @@ __device__ __forceinline__ Q8Request q8_request(const Q8Params& p, int r, bool* 
     x.q0 = r * p.s_q;
     x.n = p.s_q;
   }
-  x.len = max(p.seqlens[r], 0);
+  x.len = min(max(p.seqlens[r], 0), 0x7FFFFFFF - 256);   // the kernels round lengths up to blocks
   x.prefix = p.prefix ? p.prefix[r] : 0;
   return x;
 }

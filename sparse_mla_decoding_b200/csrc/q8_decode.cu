@@ -51,7 +51,6 @@ namespace {
 constexpr int kPartRows = kQ8PartRows;    // rows of a partial slot
 constexpr int kBatch = 16;                // visits whose table entries a warp reads at once
 constexpr int kRing = 2 * kBatch;         // and keeps
-constexpr int kSpanTokens = 16;           // document bounds are scanned up to this many new tokens
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Warps of a CTA (8 rows take 168 registers at d = 128 and 128 at d = 64, 16 rows up
@@ -78,7 +77,7 @@ constexpr int kRequests = 8;              // requests whose Work a warp keeps (a
 // so that every request with new tokens gets its outputs written.
 __device__ __forceinline__ void block_span(const Q8Params& p, const Q8Request& x, int& first, int& count) {
   int lo = 0, hi = x.len;
-  if (p.docs && x.n <= kSpanTokens) {
+  if (p.docs && x.n <= kQ8SpanTokens) {
     lo = x.len;
     hi = 0;
     for (int t = 0; t < x.n; ++t) {
@@ -543,8 +542,8 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
           if (t < x.n) {
             q8_visible(p, x, t, lo, hi);
             if (p.slopes && g == 0)
-            sm.bias[warp][8 * nt + 2 * c + i] =
-                make_float2((float)(x.len - x.n + t), p.slopes[head * p.group + hh] * kLog2e);
+              sm.bias[warp][8 * nt + 2 * c + i] =
+                  make_float2((float)(x.len - x.n + t), p.slopes[head * p.group + hh] * kLog2e);
             all_lo = max(all_lo, lo);
             all_hi = min(all_hi, hi);
           }

@@ -680,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       }
     }
   }
+  // a wait that gave up did so 2 s after the last product was issued: none is in flight
   __syncthreads();
   if (warp == 12) {
     tc_fence_after();
@@ -693,10 +694,14 @@ template <int D, bool kInt8, bool kMods>
 cudaError_t launch_as(const Q8Params& p, cudaStream_t stream) {
   constexpr int kBytes = sizeof(PrefillShared<D>) + 1024;
   // a register split above what the CTA is launched with would wait for ever
-  static const int regs = [] {
+  static std::atomic<int> known{0};
+  int regs = known.load(std::memory_order_relaxed);
+  if (regs == 0) {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, q8_prefill_kernel<D, kInt8, kMods>) == cudaSuccess ? at.numRegs : 0;
-  }();
+    if (const cudaError_t e = cudaFuncGetAttributes(&at, q8_prefill_kernel<D, kInt8, kMods>); e != cudaSuccess)
+      return e;
+    known.store(regs = at.numRegs, std::memory_order_relaxed);
+  }
   if (regs * kThreads < Split::kAll) return cudaErrorInvalidConfiguration;
   static SharedLimit limit;
   if (const cudaError_t e = raise_shared_limit(limit, (const void*)q8_prefill_kernel<D, kInt8, kMods>, kBytes);

@@ -30,7 +30,13 @@ def build(q_lens, lens, h_q, h_kv, d, kind, seed, poison=True):
     return dict(q=q, kc=kc, vc=vc, ks=ks, vs=vs, table=table, lens=lens, cu=cu, k=k, v=v)
 
 
+LONG = 1 << 20      # more than any call's tokens: picks the kernel for long prompts
+
+
 def call(x, four_d=None, **kw):
+    """Unless a test says which, the kernel for long prompts from 33 rows of a request on."""
+    rows = int(np.diff(x["cu"]).max()) * (x["q"].shape[1] // x["kc"].shape[1])
+    kw.setdefault("max_seqlen_q", LONG if rows > 32 else 1)
     import sparse_mla_decoding_b200 as smla
     dev = {n: x[n].cuda() if isinstance(x[n], torch.Tensor) else torch.from_numpy(x[n]).cuda()
            for n in ("q", "kc", "vc", "ks", "vs", "table", "lens", "cu")}
@@ -51,9 +57,12 @@ def reference(x, **kw):
 
 
 def check(x, **kw):
-    o, lse, (status, raw) = call(x, **kw)
-    assert status == 0, f"flags {raw:#x}"
-    U.compare(o, lse, reference(x, **kw))
+    """By both kernels, and by the one that the sizes pick."""
+    ref = reference(x, **kw)
+    for hint in [None, 1, LONG] if "max_seqlen_q" not in kw else [kw["max_seqlen_q"]]:
+        o, lse, (status, raw) = call(x, **{**kw, "max_seqlen_q": hint})
+        assert status == 0, f"flags {raw:#x}"
+        U.compare(o, lse, ref)
     return o, lse
 
 

@@ -69,7 +69,8 @@ def test_bad_writes(change):
                                     dict(lse=None), dict(ws=None), dict(h_q=7), dict(h_q=0), dict(batch=-1),
                                     dict(cols=0), dict(total=-1), dict(total=1 << 31), dict(total=1 << 30, h_q=8),
                                     dict(causal=2), dict(hint=-1), dict(cu=None), dict(cu=None, s_q=3),
-                                    dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")),
+                                    dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")), dict(cap=1e-30), dict(cap=1e30),
+                                    dict(scale=1e-40),
                                     dict(scale=float("inf")), dict(prefix=FAKE, causal=0), dict(qts=1025),
                                     dict(qhs=-8), dict(q=ctypes.c_void_p(0x10002)), dict(o=ctypes.c_void_p(0x10008)),
                                     dict(ws=ctypes.c_void_p(0x10010)), dict(docs=ctypes.c_void_p(0x10004))])
