@@ -251,21 +251,21 @@ int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64
   p.lse = lse;
   p.status = status;
   const bool int8 = cache->format == SMLA_Q8_INT8;
-  if (!smla::q8_decode_pays(batch, cache->h_kv, p.group, total_q, max_seqlen_q, doc_bounds != nullptr, sms)) {
-    const cudaError_t e = smla::launch_q8_prefill(p, int8, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? SMLA_OK : smla::cuda_failure(e);
-  }
-  CUtensorMap k_map, v_map;
-  if (int rc = tile_map(&k_map, cache->k_cache, cache, cache->k_block_stride)) return rc;
-  if (int rc = tile_map(&v_map, cache->v_cache, cache, cache->v_block_stride)) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace_ptr);
-  const int rows = (int)std::min<int64_t>(std::min<int64_t>(max_seqlen_q, total_q) * p.group, 0x7FFFFFFF);
   smla::Q8Scratch scratch;
   scratch.o = reinterpret_cast<float*>(ws);
   scratch.cta_o = reinterpret_cast<float*>(ws + wl.cta_o_off);
   scratch.lse = reinterpret_cast<float*>(ws + wl.lse_off);
   scratch.cta_lse = reinterpret_cast<float*>(ws + wl.cta_lse_off);
   scratch.meta = reinterpret_cast<int32_t*>(ws + wl.meta_off);
+  const int rows = (int)(std::min<int64_t>(max_seqlen_q, total_q) * p.group);   // below 2^31, as total_q * h_q is
+  if (!smla::q8_decode_pays(batch, cache->h_kv, p.group, total_q, max_seqlen_q, doc_bounds != nullptr, sms)) {
+    const cudaError_t e = smla::launch_q8_prefill(p, int8, rows, scratch, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SMLA_OK : smla::cuda_failure(e);
+  }
+  CUtensorMap k_map, v_map;
+  if (int rc = tile_map(&k_map, cache->k_cache, cache, cache->k_block_stride)) return rc;
+  if (int rc = tile_map(&v_map, cache->v_cache, cache, cache->v_block_stride)) return rc;
   const cudaError_t e = smla::launch_q8_decode(p, int8, rows, k_map, v_map, scratch, sms,
                                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SMLA_OK : smla::cuda_failure(e);

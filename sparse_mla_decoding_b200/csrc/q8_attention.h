@@ -21,26 +21,29 @@ constexpr int64_t kQ8MinVisits = 4;      // least blocks of a CTA's range
 // to leave out blocks that none of them sees.
 constexpr int kQ8SpanTokens = 16;
 
-// Which kernel.  Over equally long requests the decode kernel spreads its 16-row tiles
-// over all SMs and takes t = tiles / SMs units of time; the tensor-core kernel takes
-// waves = ceil(CTAs of 256 rows / SMs) of some 2 units each.  They cross at t between
-// 1.8 waves (rows that fill half a CTA) and 2.4.  Measured, decode against tensor
-// cores, e4m3, d = 128, 32 heads over 8: 1 request of 60000 tokens, t / waves = 0.22:
-// 92 against 764 us, 1.73: 591 against 991; 1 of 8192, 1.73: 95 against 143, 3.46: 174
-// against 144; 32 of 4096, 1.73: 101 against 121, 2.6: 142 against 121; d = 64: 8 of
-// 4096, 1.73: 44 against 53, 3.46: 74 against 53.
+// Which kernel.  Both spread their work over the SMs; a tile of 16 rows costs the decode
+// kernel 0.4 times what 256 rows (or a part of them) cost the tensor-core kernel, whose
+// CTAs take some 10 us before and after.  So up to two tiles in place of a CTA go to the
+// decode kernel, and so few tiles that they are over before a CTA of the other is.
+// Measured, decode against tensor cores, us, 32 heads over 8, d = 128:
+//   rows of a request      16          32          48          64         128
+//   32 of 4096 tokens   62 / 123   101 / 123   143 / 123   183 / 124
+//   4 of 8192           29 / 42     41 / 42     53 / 42     64 / 42    110 / 43
+//   1 of 60000          39 / 68     58 / 68     76 / 69     92 / 68    162 / 69
+//   1 of 8192           17 / 26     21 / 26     25 / 26     26 / 26     36 / 26
+//   1 of 8192, 1 head   15 / 30     15 / 30     15 / 31     15 / 30     17 / 30
 inline bool q8_decode_pays(int64_t batch, int64_t h_kv, int64_t group, int64_t total_q, int64_t max_q, bool docs,
                            int sms) {
   if (max_q > total_q || (docs && max_q > kQ8SpanTokens)) return false;
-  const auto tiles = [&](int64_t rows) {              // at most
-    return std::min(batch * ((max_q * group + rows - 1) / rows), total_q * group / rows + batch) * h_kv;
+  const auto tiles = [&](int64_t rows) {              // at most, of one head
+    return std::min(batch * ((max_q * group + rows - 1) / rows), total_q * group / rows + batch);
   };
-  const int64_t waves = (tiles(256) + sms - 1) / sms;
-  return 4 * tiles(16) <= 7 * waves * sms;
+  return tiles(16) <= 2 * tiles(256) || 6 * tiles(16) * h_kv <= sms;
 }
 
 // Partials of the decode kernel: two slots of kQ8PartRows rows for each warp and for
-// each CTA.
+// each CTA.  The tensor-core kernel has its slots of 256 rows in `o` and `lse` (two for
+// each SM) and one entry of `meta` for each 256 rows that several CTAs share.
 struct Q8Scratch {
   float *o, *cta_o;                      // [2 warps or CTAs][kQ8PartRows][d], normalised
   float *lse, *cta_lse;                  // [2 warps or CTAs][kQ8PartRows], log2
@@ -52,8 +55,10 @@ struct Q8Scratch {
 cudaError_t launch_q8_decode(const Q8Params& p, bool int8, int rows, const CUtensorMap& k_map,
                              const CUtensorMap& v_map, const Q8Scratch& scratch, int ctas, cudaStream_t stream);
 
-// The tensor-core kernel for many new tokens: no scratch, one CTA per 256 rows.
-cudaError_t launch_q8_prefill(const Q8Params& p, bool int8, cudaStream_t stream);
+// The tensor-core kernel for many new tokens, one CTA per 256 rows or, where these would
+// not fill the SMs, several; `rows` as above.
+cudaError_t launch_q8_prefill(const Q8Params& p, bool int8, int64_t rows, const Q8Scratch& scratch, int sms,
+                              cudaStream_t stream);
 
 // Raises a kernel's shared memory limit, once per device context (`done`, one per
 // kernel, remembers the contexts; after a device reset the context is a new one).

@@ -31,10 +31,21 @@
 // the products are one per block parity: the one of block i + 2 cannot be reached
 // before all four warps are done with block i.
 //
-// Bound, for 256 rows x 128 keys at d = 128: tensor 2 x (768 + 512) clocks,
-// exponentials 2048 clocks of the special function units.
+// Where the rows do not fill the SMs (a chunk of one request over a long context),
+// several CTAs (z) share 256 rows: each takes an equal part of the blocks and leaves a
+// normalised fp32 partial, and q8_join_kernel joins them by their lse.  One request, 8
+// KV heads, groups of 4, d = 128, alone and shared: 128 tokens on 60000 991 and 136 us, 256
+// on 8192 143 and 54, 64 on 8192 141 and 35.
+//
+// Bound, for 256 rows x 64 keys at d = 128: 1330 clocks of the tensor cores, 1024 of
+// the special function units with all exponentials there (a quarter is on the FMA
+// pipe).  A step takes 1900 (long loops) to 2300 clocks: the chain of a softmax warp
+// from S to P is longer than the products of the other tile.  A CTA takes about 8 us
+// beside its steps (finding its request, Q, the output), which is what short prompts
+// and documents wait for.  8192 tokens on 8192, 32 heads: 1.46 ms, 1.13 PFLOP/s.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "q8_attention.h"
@@ -57,6 +68,9 @@ struct Split {
   static constexpr int kAll = 256 * kSoftmax + 128 * kProducer + 128 * kMma;
   static_assert(kAll <= 65536, "the split must fit what the CTA was launched with");
 };
+constexpr int kMostSplits = 32;           // CTAs that share 256 rows
+constexpr int kLeastBlocks = 4;           // cache blocks of each
+constexpr int kWhole = -1, kNothing = -2;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct BlockScales {
@@ -80,6 +94,7 @@ struct PrefillShared {                    // at a 1024-byte boundary
   Q8Request x;
   int64_t row0, rows_all;
   bool bad;                               // its offsets
+  int part;                               // where the result goes: kWhole, kNothing or a partial's slot
 };
 
 __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
@@ -240,12 +255,15 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
 }  // namespace
 
 template <int D, bool kInt8, bool kMods>
-__global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_constant__ Q8Params p) {
+__global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_constant__ Q8Params p, Q8Scratch scratch) {
   constexpr int kStage = kBlk * D * 2;
   extern __shared__ uint8_t raw[];
   PrefillShared<D>& sm = *reinterpret_cast<PrefillShared<D>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int head = blockIdx.y;
+  const bool first_cta = blockIdx.x + blockIdx.y + blockIdx.z == 0;
+  int32_t* const meta = scratch.meta + 8 * ((size_t)blockIdx.x * p.h_kv + head);
+  if (gridDim.z > 1 && blockIdx.z == 0 && tid == 0) meta[0] = 0;
 
   // ---- which rows: request r may hold the items from cu[r] * group / 256 + r on
   // (one more than its rows fill); the last items, whose tokens see most, first
@@ -259,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     Q8Request mine{0, 0, 0, 0};
     if (i < p.batch) {
       mine = q8_request(p, i, &bad);
-      if (bad && blockIdx.x + blockIdx.y == 0) report_status(p.status, kStatusBadSchedule);
+      if (bad && first_cta) report_status(p.status, kStatusBadSchedule);
       const int64_t c = p.cu_q ? max(p.cu_q[i], 0) : (int64_t)i * p.s_q;
       before = c * p.group / (2 * kTileRows) + i <= item;
     }
@@ -269,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       sm.bad = bad;
     }
     if (r == i0 - 1) r += c;
-    if (c < kThreads && blockIdx.x + blockIdx.y > 0) break;   // the first CTA looks them all over
+    if (c < kThreads && !first_cta) break;   // the first CTA looks them all over
   }
   if (r < 0) return;
   __syncthreads();
@@ -297,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     sm.hi = 0;
     sm.row0 = row0;
     sm.rows_all = rows_all;
+    sm.part = kWhole;
     mbar_init_fence();
   }
   if (warp == 12) {
@@ -324,10 +343,22 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
   const int end = (int)min((int64_t)min(sm.hi, 0x7FFFFFFF - 256), (int64_t)p.max_blocks * kBlk);
-  const int first = sm.lo / kBlk;                     // blocks [first, first + blocks)
-  const int blocks = sm.lo < end ? (end + kBlk - 1) / kBlk - first : 0;
+  int first = sm.lo / kBlk;                           // blocks [first, first + blocks)
+  int blocks = sm.lo < end ? (end + kBlk - 1) / kBlk - first : 0;
   if (tid == 0 && sm.hi > (int64_t)p.max_blocks * kBlk) report_status(p.status, kStatusBadBlockTable);
 
+  if (gridDim.z > 1) {                                // the blocks in equal parts over z
+    const int per = max((blocks + (int)gridDim.z - 1) / (int)gridDim.z, kLeastBlocks);
+    const int parts = max((blocks + per - 1) / per, 1), z = blockIdx.z;
+    if (tid == 0) {
+      sm.part = z >= parts ? kNothing : parts == 1 ? kWhole : ((int)blockIdx.x * p.h_kv + head) * (int)gridDim.z + z;
+      if (z == 0 && parts > 1)
+        *reinterpret_cast<int4*>(meta) = make_int4(parts, x.q0, (int)row0, (int)rows_all);
+    }
+    __syncthreads();
+    first += z * per;
+    blocks = max(min(per, blocks - z * per), 0);
+  }
   if (warp < 8) {
     // ================================ softmax ================================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split::kSoftmax));
@@ -489,12 +520,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
       // need is worked out anew: its registers are S's.
       if (ok && blocks > 0) ok = bar_wait_warp(&sm.odone[w][(blocks - 1) & 1], ((blocks - 1) >> 1) & 1, p.status);
       tc_fence_after();
-      if (ok) {
+      if (ok && static_cast<const volatile int&>(sm.part) != kNothing) {
         int me;
         asm volatile("mov.u32 %0, %%tid.x;" : "=r"(me));
         const volatile PrefillShared<D>& v_sm = sm;
         const int64_t row0 = v_sm.row0, rows_all = v_sm.rows_all;
-        const int q0 = v_sm.x.q0, head = blockIdx.y, lane = me & 31, warp = me >> 5;
+        const int q0 = v_sm.x.q0, part = v_sm.part, head = blockIdx.y, lane = me & 31, warp = me >> 5;
         const bool none = m == -INFINITY && !(l != l);
         const float inv = none ? 0.f : ex2(sm.base_log2) / l;
         const uint32_t qs = smem_u32(sm.q[warp >> 2]);
@@ -503,6 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
           float o[32];
           tmem_ld32(o_addr + c, o);
           tmem_wait_ld();
+          if (part >= 0) {
+            float4* dst = reinterpret_cast<float4*>(scratch.o + ((int64_t)part * 2 * kTileRows + me) * D + c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+            continue;
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t v[4];
@@ -515,19 +553,23 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
             sts128(qs + operand_at(me & 127, c / 8 + k), v[0], v[1], v[2], v[3]);
           }
         }
-        int at = -1;                                  // this thread's row of o and lse
-        if (row0 + me < rows_all) {
-          const int t = (int)(row0 + me) / p.group;
-          at = (q0 + t) * p.h_q + head * p.group + (int)(row0 + me) - t * p.group;
-          p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
-        }
-        __syncwarp();
-        const int sub = lane / kRowLanes<D>, chunk = lane % kRowLanes<D>;
+        if (part >= 0) {
+          scratch.lse[(int64_t)part * 2 * kTileRows + me] = none ? -INFINITY : m + log2f(l);
+        } else {
+          int at = -1;                                  // this thread's row of o and lse
+          if (row0 + me < rows_all) {
+            const int t = (int)(row0 + me) / p.group;
+            at = (q0 + t) * p.h_q + head * p.group + (int)(row0 + me) - t * p.group;
+            p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+          }
+          __syncwarp();
+          const int sub = lane / kRowLanes<D>, chunk = lane % kRowLanes<D>;
 #pragma unroll 4
-        for (int k = 0; k < 32; k += 32 / kRowLanes<D>) {
-          const int to = __shfl_sync(0xffffffffu, at, k + sub);
-          const uint4 v = lds128(qs + operand_at(32 * (warp & 3) + k + sub, chunk));
-          if (to >= 0) reinterpret_cast<uint4*>(p.o + (int64_t)to * D)[chunk] = v;
+          for (int k = 0; k < 32; k += 32 / kRowLanes<D>) {
+            const int to = __shfl_sync(0xffffffffu, at, k + sub);
+            const uint4 v = lds128(qs + operand_at(32 * (warp & 3) + k + sub, chunk));
+            if (to >= 0) reinterpret_cast<uint4*>(p.o + (int64_t)to * D)[chunk] = v;
+          }
         }
       }
       tc_fence_before();
@@ -688,10 +730,56 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
   }
 }
 
+// Joins the parts of CTAs that shared 256 rows: eight lanes a row, a lane's values d =
+// 32 k + 4 (lane % 8) and the next three.
+constexpr int kJoinRows = 16;             // rows of a CTA
+template <int D>
+__global__ void __launch_bounds__(8 * kJoinRows) q8_join_kernel(const __grid_constant__ Q8Params p, Q8Scratch scratch,
+                                                               int splits) {
+  constexpr int kV = D / 32;
+  pdl_wait_primary();
+  const int4 ma = *reinterpret_cast<const int4*>(scratch.meta + 8 * (size_t)blockIdx.x);
+  const int parts = ma.x, lane8 = threadIdx.x & 7, in_tile = blockIdx.y * kJoinRows + (threadIdx.x >> 3);
+  const int64_t row = (int64_t)ma.z + in_tile;
+  if (parts == 0 || row >= ma.w) return;
+  const int64_t at0 = (int64_t)blockIdx.x * splits * 2 * kTileRows + in_tile;
+  float top = -INFINITY, sum = 0.f;
+  for (int s = 0; s < parts; ++s) top = fmaxf(top, scratch.lse[at0 + (int64_t)s * 2 * kTileRows]);
+  float4 o[kV];
+#pragma unroll
+  for (int k = 0; k < kV; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const int64_t at = at0 + (int64_t)s * 2 * kTileRows;
+    const float lse = scratch.lse[at], w = lse == -INFINITY ? 0.f : ex2(lse - top);
+    sum += w;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      const float4 x = reinterpret_cast<const float4*>(scratch.o + at * D)[8 * k + lane8];
+      if (lse == -INFINITY) continue;                 // what stands there is no number
+      o[k].x = fmaf(w, x.x, o[k].x);
+      o[k].y = fmaf(w, x.y, o[k].y);
+      o[k].z = fmaf(w, x.z, o[k].z);
+      o[k].w = fmaf(w, x.w, o[k].w);
+    }
+  }
+  const int t = (int)row / p.group, head = blockIdx.x % p.h_kv, hq = head * p.group + (int)row - t * p.group;
+  const int64_t to = (int64_t)(ma.y + t) * p.h_q + hq;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int k = 0; k < kV; ++k) {
+    __nv_bfloat162 a = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
+    __nv_bfloat162 b = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
+    reinterpret_cast<uint2*>(p.o + to * D)[8 * k + lane8] =
+        make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+  }
+  if (lane8 == 0) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
 namespace {
 
 template <int D, bool kInt8, bool kMods>
-cudaError_t launch_as(const Q8Params& p, cudaStream_t stream) {
+cudaError_t launch_as(const Q8Params& p, int64_t rows, const Q8Scratch& scratch, int sms, cudaStream_t stream) {
   constexpr int kBytes = sizeof(PrefillShared<D>) + 1024;
   // a register split above what the CTA is launched with would wait for ever
   static std::atomic<int> known{0};
@@ -709,20 +797,40 @@ cudaError_t launch_as(const Q8Params& p, cudaStream_t stream) {
     return e;
   const int64_t items = (int64_t)p.total_q * p.group / (2 * kTileRows) + p.batch;
   if (items > 0x7FFFFFFF || p.h_kv > 65535) return cudaErrorInvalidConfiguration;
-  q8_prefill_kernel<D, kInt8, kMods><<<dim3((unsigned)items, (unsigned)p.h_kv), kThreads, kBytes, stream>>>(p);
-  return cudaGetLastError();
+  // CTAs with rows, as far as the host knows, and how many share one's rows so that
+  // they fill the SMs; the workspace has slots for two times the SMs
+  const int64_t each = (rows + 2 * kTileRows - 1) / (2 * kTileRows);
+  const int64_t busy = std::max<int64_t>(each < items ? std::min(p.batch * each, items) : items, 1) * p.h_kv;
+  const int splits =
+      (int)std::max<int64_t>(std::min({sms / busy, 2 * sms / (items * p.h_kv), (int64_t)kMostSplits}), 1);
+  q8_prefill_kernel<D, kInt8, kMods>
+      <<<dim3((unsigned)items, (unsigned)p.h_kv, (unsigned)splits), kThreads, kBytes, stream>>>(p, scratch);
+  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess || splits == 1) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(items * p.h_kv), 2 * kTileRows / kJoinRows);
+  cfg.blockDim = dim3(8 * kJoinRows);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, q8_join_kernel<D>, p, scratch, splits);
 }
 
 template <int D, bool kInt8>
-cudaError_t launch(const Q8Params& p, cudaStream_t stream) {
-  return p.cap > 0.f || p.slopes ? launch_as<D, kInt8, true>(p, stream) : launch_as<D, kInt8, false>(p, stream);
+cudaError_t launch(const Q8Params& p, int64_t rows, const Q8Scratch& scratch, int sms, cudaStream_t stream) {
+  return p.cap > 0.f || p.slopes ? launch_as<D, kInt8, true>(p, rows, scratch, sms, stream)
+                                 : launch_as<D, kInt8, false>(p, rows, scratch, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_q8_prefill(const Q8Params& p, bool int8, cudaStream_t stream) {
-  if (p.d == 128) return int8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
-  return int8 ? launch<64, true>(p, stream) : launch<64, false>(p, stream);
+cudaError_t launch_q8_prefill(const Q8Params& p, bool int8, int64_t rows, const Q8Scratch& scratch, int sms,
+                              cudaStream_t stream) {
+  if (p.d == 128)
+    return int8 ? launch<128, true>(p, rows, scratch, sms, stream) : launch<128, false>(p, rows, scratch, sms, stream);
+  return int8 ? launch<64, true>(p, rows, scratch, sms, stream) : launch<64, false>(p, rows, scratch, sms, stream);
 }
 
 }  // namespace smla

@@ -219,7 +219,8 @@ def test_rows_behind_the_last_request_are_left(n):
     o = torch.full((2 * n + 7, 8, 128), 3.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((2 * n + 7, 8), 5.0, device="cuda")
     smla.gqa_attention_with_kvcache(q, x["kc"].cuda(), x["vc"].cuda(), x["ks"].cuda(), x["vs"].cuda(),
-                                    *(torch.from_numpy(x[k]).cuda() for k in ("table", "lens", "cu")), out=(o, lse))
+                                    *(torch.from_numpy(x[k]).cuda() for k in ("table", "lens", "cu")), out=(o, lse),
+                                    max_seqlen_q=1 if n == 1 else LONG)
     U.compare(o[:2 * n], lse[:2 * n], reference(x))
     assert (o[2 * n:] == 3).all() and (lse[2 * n:] == 5).all()
 
@@ -280,7 +281,8 @@ def test_blocks_past_two_gigabytes(n):
     table[:, :4] += nb - used
     args = [torch.from_numpy(x[k]).cuda() for k in ("lens", "cu")]
     o, lse = smla.gqa_attention_with_kvcache(x["q"].cuda(), big["kc"], big["vc"], big["ks"], big["vs"], table, args[0],
-                                             cu_seqlens_q=args[1], check_device_status=True)
+                                             cu_seqlens_q=args[1], max_seqlen_q=1 if n == 1 else LONG,
+                                             check_device_status=True)
     U.compare(o, lse, reference(x))
     k = torch.randn(3, 8, 128, device="cuda").to(torch.bfloat16)
     cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
@@ -294,6 +296,34 @@ def test_blocks_past_two_gigabytes(n):
     assert torch.equal(before, big["kc"][nb - used:])
 
 
+@pytest.mark.parametrize("kind,d", [("e4m3", 128), ("int8", 64)])
+@pytest.mark.parametrize("mods", ["", "docs", "cap prefix slopes"])
+def test_rows_shared_by_several_ctas(mods, kind, d):
+    """Few row tiles over long lengths: parts that some or all rows do not see, a request too
+    short to be shared, lengths that end inside a block, rows that end inside a tile."""
+    q_lens, lens = [150, 3, 20, 140], [4000, 90, 2777, 140]
+    x = build(q_lens, lens, 8, 2, d, kind, 1700 + d)
+    kw = {}
+    if "docs" in mods:
+        rng = np.random.default_rng(d)
+        total = sum(q_lens)
+        lo = rng.integers(0, 2600, total)
+        docs = np.stack([lo, lo + rng.integers(0, 900, total)], 1).astype(np.int32)
+        docs[:40] = [3900, 4100]
+        docs[155:160] = [700, 700]
+        kw["doc_bounds"] = docs
+    if "cap" in mods:
+        kw.update(softcap=5.0, prefix_lens=np.array([3950, 0, 0, 100], np.int32),
+                  alibi_slopes=(0.02 * 2.0 ** -np.arange(8)).astype(np.float32))
+    check(x, **kw)
+
+
+def test_more_rows_than_workspace_slots():
+    """As many CTAs as fill the SMs: none is shared, and the workspace is not used."""
+    x = build([130] * 40, [200 + i for i in range(40)], 8, 4, 64, "e4m3", 1800)
+    check(x, max_seqlen_q=130)
+
+
 def test_repeated_calls_are_bitwise_equal():
     x = build([1, 2, 30], [5000, 900, 300], 16, 2, 128, "e4m3", 1400)
     first = call(x)
@@ -302,7 +332,8 @@ def test_repeated_calls_are_bitwise_equal():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
-def test_a_captured_call_replays_on_new_inputs():
+@pytest.mark.parametrize("hint", [1, LONG])
+def test_a_captured_call_replays_on_new_inputs(hint):
     """A graph keeps its own scratch: replays beside eager calls, on another stream, give the eager results."""
     import sparse_mla_decoding_b200 as smla
     x = build([1, 2, 30], [3000, 900, 300], 16, 2, 128, "e4m3", 1500)
@@ -311,7 +342,7 @@ def test_a_captured_call_replays_on_new_inputs():
 
     def run():
         return smla.gqa_attention_with_kvcache(t["q"], t["kc"], t["vc"], t["ks"], t["vs"], t["table"], t["lens"],
-                                               cu_seqlens_q=t["cu"])
+                                               cu_seqlens_q=t["cu"], max_seqlen_q=hint)
     run()
     torch.cuda.synchronize()
     graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
@@ -331,7 +362,8 @@ def test_a_captured_call_replays_on_new_inputs():
     assert smla.paged_status()[0] == 0
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("hint", [1, LONG])
+def test_two_streams_at_once(hint):
     import sparse_mla_decoding_b200 as smla
     xs = [build([1, 1], [4000, 70], 8, 2, 128, kind, 1600) for kind in KINDS]
     ts = [{n: (x[n] if isinstance(x[n], torch.Tensor) else torch.from_numpy(x[n])).cuda()
@@ -343,7 +375,7 @@ def test_two_streams_at_once():
         for i, (t, s) in enumerate(zip(ts, streams)):
             with torch.cuda.stream(s):
                 outs[i].append(smla.gqa_attention_with_kvcache(t["q"], t["kc"], t["vc"], t["ks"], t["vs"], t["table"],
-                                                               t["lens"], cu_seqlens_q=t["cu"]))
+                                                               t["lens"], cu_seqlens_q=t["cu"], max_seqlen_q=hint))
     torch.cuda.synchronize()
     for x, got in zip(xs, outs):
         U.compare(*got[0], reference(x))
