@@ -255,7 +255,8 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
 }  // namespace
 
 template <int D, bool kInt8, bool kMods>
-__global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_constant__ Q8Params p, Q8Scratch scratch) {
+__global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_constant__ Q8Params p,
+                                                                  Q8Scratch scratch) {
   constexpr int kStage = kBlk * D * 2;
   extern __shared__ uint8_t raw[];
   PrefillShared<D>& sm = *reinterpret_cast<PrefillShared<D>*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
