@@ -464,7 +464,9 @@ size_t smla_gqa_workspace_bytes(int head_dim, int device);
  *   lse          : device float32 [total_q][h_q], natural log
  *   workspace    : device, >= smla_gqa_workspace_bytes, 256-byte aligned; calls
  *                  that may run at the same time need workspaces of their own
- *   status       : as for smla_quantize_kv_blocks
+ *   status       : as for smla_quantize_kv_blocks; flagged too, and nothing
+ *                  written, where the kernel for few tokens would have to read
+ *                  2^31 blocks or more
  * h_q is a multiple of h_kv, below 2^20; total_q * h_q < 2^31.  Rows of q that
  * belong to no request are not read and their outputs not written.  A position
  * whose block lies outside the table or the cache is skipped and flagged; so is

@@ -556,7 +556,7 @@ def _block_table(t: torch.Tensor, index: int) -> Tuple[int, int]:
 
 def _on_device(index: int, call, *args) -> int:
     """call(*args) with device `index` current."""
-    back = torch.cuda.current_device()
+    back = torch._C._cuda_getDevice()
     if back == index:
         return call(*args)
     torch.cuda.set_device(index)
@@ -631,10 +631,34 @@ def _q8_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tenso
                     kss[0], vss[0], h_kv, d, fmt)
 
 
-def _rows16(t: torch.Tensor) -> torch.Tensor:
-    """t [n, h, d] with dense rows that 16-byte loads can read; a copy where it has none."""
-    a, b, c = t.stride()
-    return t if c == 1 and a % 8 == 0 and b % 8 == 0 and t.data_ptr() % 16 == 0 else t.contiguous()
+def _rows16(t: torch.Tensor, n: int, h: int, d: int) -> Tuple[torch.Tensor, int, int]:
+    """t [.., h, d] of n tokens with dense rows that 16-byte loads can read (a copy where it
+    has none), and the strides of its tokens and heads."""
+    s = t.stride()
+    if len(s) == 3:
+        a, b, c = s
+    else:                            # [requests, tokens each, h, d]
+        r, a, b, c = s
+        each = t.shape[1]
+        if each == 1:
+            a = r
+        elif r != each * a and n > each:
+            c = 0                    # no one stride leads through the tokens
+    if (a | b) & 7:                  # a lone token's or head's stride is free to say anything
+        a, b = h * d if n == 1 else a, d if h == 1 else b
+    if c == 1 and not (a | b) & 7 and not t.data_ptr() & 15:
+        return t, a, b
+    return t.clone(memory_format=torch.contiguous_format), h * d, d
+
+
+_gqa_bytes: dict = {}                # (head_dim, device): fixed by the device
+
+
+def _gqa_workspace(d: int, index: int) -> int:
+    n = _gqa_bytes.get((d, index))
+    if n is None:
+        n = _gqa_bytes[d, index] = lib().smla_gqa_workspace_bytes(d, index)
+    return n
 
 
 def quantize_kv_blocks(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -665,10 +689,10 @@ def quantize_kv_blocks(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, 
     cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", index)
     new_seqlens = _i32_vector(new_seqlens, b, "new_seqlens", index)
     cu_new = _i32_vector(cu_new, b + 1, "cu_new", index)
-    k, v = _rows16(k), _rows16(v)
-    ks, vs = k.stride(), v.stride()
+    k, kts, khs = _rows16(k, *shape)
+    v, vts, vhs = _rows16(v, *shape)
     word = _paged_word(index)
-    rc = _on_device(index, lib().smla_quantize_kv_blocks, k.data_ptr(), v.data_ptr(), ks[0], ks[1], vs[0], vs[1],
+    rc = _on_device(index, lib().smla_quantize_kv_blocks, k.data_ptr(), v.data_ptr(), kts, khs, vts, vhs,
                     shape[0], ctypes.byref(cache), block_table.data_ptr(), cols, b, cache_seqlens.data_ptr(),
                     new_seqlens.data_ptr(), cu_new.data_ptr(), _ptr(word), _raw_stream(index))
     if rc:
@@ -729,19 +753,18 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     h_q = shape[-2]
     if h_q < 1 or h_q % cache.h_kv:
         _bad("h_q must be a multiple of h_kv")
-    s_q, cu = 0, None
+    s_q, cu, total = 0, None, shape[0]
     if cu_seqlens_q is None:
         if shape[0] != b:
             _bad(f"q must hold {b} requests")
         s_q = shape[1]
+        total = b * s_q
         if max_seqlen_q is None:
             max_seqlen_q = s_q
-        q = q.flatten(0, 1)
     else:
         cu_seqlens_q = _i32_vector(cu_seqlens_q, b + 1, "cu_seqlens_q", index)
         cu = cu_seqlens_q.data_ptr()
-    q = _rows16(q)
-    total = q.shape[0]
+    rows, q_tok, q_head = _rows16(q, total, h_q, d)
     cache_seqlens = _i32_vector(cache_seqlens, b, "cache_seqlens", index)
     if alibi_slopes is not None:
         if alibi_slopes.dtype != torch.float32 or alibi_slopes.shape != (h_q,) or alibi_slopes.get_device() != index:
@@ -766,7 +789,7 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         if not 2.0 ** -126 <= scale < 2.0 ** 127:
             _bad("softmax_scale must be > 0 and finite (as a normal float32)")
     if out is None:
-        o, lse = q.new_empty(shape), k_scale.new_empty(shape[:-1])
+        o, lse = torch.empty_like(q, memory_format=torch.contiguous_format), k_scale.new_empty(*shape[:-1])
     else:
         o, lse = out
         for name, t, dt, sh in (("o", o, torch.bfloat16, shape), ("lse", lse, torch.float32, shape[:-1])):
@@ -774,8 +797,7 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                 _bad(f"out: {name} must be contiguous {dt} {list(sh)} on cuda:{index}")
         if o.data_ptr() % 16:
             _bad("out: o must be 16-byte aligned")
-    L = lib()
-    nbytes = L.smla_gqa_workspace_bytes(d, index)
+    nbytes = _gqa_workspace(d, index)
     if workspace is None:
         word, scratch = _paged_word(index), k_scale.new_empty(nbytes // 4)
         at, room = scratch.data_ptr(), nbytes
@@ -785,7 +807,7 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
             _bad(f"workspace needs {256 + nbytes} bytes of uint8 on cuda:{index}")
         word, at, room = workspace, workspace.data_ptr() + 256, workspace.numel() - 256
     rc = _on_device(
-        index, L.smla_gqa_attention_with_kvcache, q.data_ptr(), q.stride(0), q.stride(1), total, h_q,
+        index, lib().smla_gqa_attention_with_kvcache, rows.data_ptr(), q_tok, q_head, total, h_q,
         ctypes.byref(cache), block_table.data_ptr(), cols, b, cache_seqlens.data_ptr(), cu, s_q,
         total if max_seqlen_q is None else int(max_seqlen_q), 1 if causal else 0, scale, softcap, _ptr(alibi_slopes),
         _ptr(prefix_lens), _ptr(doc_bounds), o.data_ptr(), lse.data_ptr(), at, room, _ptr(word), _raw_stream(index))

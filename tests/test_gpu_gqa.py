@@ -211,6 +211,32 @@ def test_strided_queries_scales_and_blocks():
     U.compare(o, lse, reference(x))
 
 
+@pytest.mark.parametrize("shape", [(1, 1), (2, 1), (1, 3), (2, 3)])
+@pytest.mark.parametrize("h_q", [1, 4])
+def test_odd_query_strides_and_alignments(shape, h_q):
+    """Queries that 16-byte loads cannot read as they are, and strides of lone dimensions."""
+    import sparse_mla_decoding_b200 as smla
+    b, s_q = shape
+    x = build([s_q] * b, [70] * b, h_q, 1, 64, "int8", 1050 + h_q)
+    q = x["q"].view(b, s_q, h_q, 64).cuda()
+    n = q.numel()
+    odd = torch.empty(n + 1, dtype=torch.bfloat16, device="cuda")[1:].view(q.shape)
+    odd.copy_(q)
+    wide = torch.empty(b, s_q, h_q, 67, dtype=torch.bfloat16, device="cuda")[..., :64]
+    wide.copy_(q)
+    turned = torch.empty(s_q, b, h_q, 64, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    turned.copy_(q)
+    lone = q.as_strided(q.shape, tuple(st if sz > 1 else 5 for sz, st in zip(q.shape, q.stride())))
+    apart = torch.empty(b, s_q + 2, h_q, 64, dtype=torch.bfloat16, device="cuda")[:, :s_q]
+    apart.copy_(q)
+    args = [x[k].cuda() for k in ("kc", "vc", "ks", "vs")] + [torch.from_numpy(x[k]).cuda() for k in ("table", "lens")]
+    ref = reference(x)
+    for t in (q, odd, wide, turned, lone, apart):
+        o, lse = smla.gqa_attention_with_kvcache(t, *args, check_device_status=True)
+        assert o.is_contiguous() and o.shape == q.shape
+        U.compare(o.view(-1, h_q, 64), lse.view(-1, h_q), ref)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_rows_behind_the_last_request_are_left(n):
     import sparse_mla_decoding_b200 as smla
