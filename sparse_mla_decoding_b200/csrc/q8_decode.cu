@@ -870,6 +870,8 @@ cudaError_t launch(const Q8Params& p, const CUtensorMap& k_map, const CUtensorMa
 template <int D, bool kInt8>
 cudaError_t launch_rows(const Q8Params& p, int rows, const CUtensorMap& k_map, const CUtensorMap& v_map,
                         const Q8Scratch& scratch, int ctas, cudaStream_t stream) {
+  // 32 requests of 4096 tokens, 8 heads, with tiles of 8 and of 16 rows: at 8 rows 56 and 58
+  // us (d = 64: 37 and 45), at 16 rows 84 and 61 (47 and 46), at 32 158 and 101 (79 and 76)
   return rows <= 8 ? launch<D, kInt8, 1>(p, k_map, v_map, scratch, ctas, stream)
                    : launch<D, kInt8, 2>(p, k_map, v_map, scratch, ctas, stream);
 }

@@ -34,8 +34,8 @@
 // Where the rows do not fill the SMs (a chunk of one request over a long context),
 // several CTAs (z) share 256 rows: each takes an equal part of the blocks and leaves a
 // normalised fp32 partial, and q8_join_kernel joins them by their lse.  One request, 8
-// KV heads, groups of 4, d = 128, alone and shared: 128 tokens on 60000 991 and 136 us, 256
-// on 8192 143 and 54, 64 on 8192 141 and 35.
+// KV heads, groups of 4, d = 128, alone and shared: 128 tokens on 60000 991 and 133 us, 256
+// on 8192 143 and 53, 64 on 8192 141 and 34.
 //
 // Bound, for 256 rows x 64 keys at d = 128: 1330 clocks of the tensor cores, 1024 of
 // the special function units with all exponentials there (a quarter is on the FMA
@@ -69,7 +69,9 @@ struct Split {
   static_assert(kAll <= 65536, "the split must fit what the CTA was launched with");
 };
 constexpr int kMostSplits = 32;           // CTAs that share 256 rows
-constexpr int kLeastBlocks = 4;           // cache blocks of each
+// Cache blocks of each, and how many are not shared at all: 64 tokens on 1000 take 20.4 us
+// with parts of 4, 22.4 with 6 and 24.3 with 8; on 300 (5 blocks) 19.6 shared, 15.5 not.
+constexpr int kLeastBlocks = 4, kAloneBlocks = 8;
 constexpr int kWhole = -1, kNothing = -2;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -349,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
   if (tid == 0 && sm.hi > (int64_t)p.max_blocks * kBlk) report_status(p.status, kStatusBadBlockTable);
 
   if (gridDim.z > 1) {                                // the blocks in equal parts over z
-    const int per = max((blocks + (int)gridDim.z - 1) / (int)gridDim.z, kLeastBlocks);
+    const int least = blocks <= kAloneBlocks ? kAloneBlocks : kLeastBlocks;
+    const int per = max((blocks + (int)gridDim.z - 1) / (int)gridDim.z, least);
     const int parts = max((blocks + per - 1) / per, 1), z = blockIdx.z;
     if (tid == 0) {
       sm.part = z >= parts ? kNothing : parts == 1 ? kWhole : ((int)blockIdx.x * p.h_kv + head) * (int)gridDim.z + z;
@@ -731,50 +734,68 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
   }
 }
 
-// Joins the parts of CTAs that shared 256 rows: eight lanes a row, a lane's values d =
-// 32 k + 4 (lane % 8) and the next three.
-constexpr int kJoinRows = 16;             // rows of a CTA
-template <int D>
-__global__ void __launch_bounds__(8 * kJoinRows) q8_join_kernel(const __grid_constant__ Q8Params p, Q8Scratch scratch,
+// Joins the parts of CTAs that shared 256 rows: kTeams teams of eight lanes a row, a
+// lane's values d = 32 k + 4 (lane % 8) and the next three.  Lane s has the weight of
+// part s, and the teams take the parts in turn.  What costs is the trips to L2: one for
+// the lse, then one for four parts of each team.  Up to eight parts have one team (512
+// tokens on 8192: 91 us, with four teams 94), more have four (64 tokens on 8192, one
+// head, 32 parts: 23 us, with one 35).
+constexpr int kJoinThreads = 256;
+static_assert(kMostSplits <= 32, "a lane for each part");
+template <int D, int kTeams>
+__global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const __grid_constant__ Q8Params p, Q8Scratch scratch,
                                                                int splits) {
+  constexpr int kLanes = 8 * kTeams;      // of a row
   constexpr int kV = D / 32;
   pdl_wait_primary();
   const int4 ma = *reinterpret_cast<const int4*>(scratch.meta + 8 * (size_t)blockIdx.x);
-  const int parts = ma.x, lane8 = threadIdx.x & 7, in_tile = blockIdx.y * kJoinRows + (threadIdx.x >> 3);
+  const int lane = threadIdx.x % kLanes, in_tile = blockIdx.y * (kJoinThreads / kLanes) + threadIdx.x / kLanes;
+  const int parts = ma.x, lane8 = lane & 7, team = lane >> 3;
   const int64_t row = (int64_t)ma.z + in_tile;
-  if (parts == 0 || row >= ma.w) return;
+  if (parts == 0 || row - threadIdx.x / kLanes >= ma.w) return;   // the CTA's first row
   const int64_t at0 = (int64_t)blockIdx.x * splits * 2 * kTileRows + in_tile;
-  float top = -INFINITY, sum = 0.f;
-  for (int s = 0; s < parts; ++s) top = fmaxf(top, scratch.lse[at0 + (int64_t)s * 2 * kTileRows]);
+  const float lse = lane < parts && row < ma.w ? scratch.lse[at0 + (int64_t)lane * 2 * kTileRows] : -INFINITY;
+  float top = lse;
+#pragma unroll
+  for (int off = kLanes / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const float w = lse == -INFINITY ? 0.f : ex2(lse - top);
+  float sum = w;
+#pragma unroll
+  for (int off = kLanes / 2; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   float4 o[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const int64_t at = at0 + (int64_t)s * 2 * kTileRows;
-    const float lse = scratch.lse[at], w = lse == -INFINITY ? 0.f : ex2(lse - top);
-    sum += w;
+  for (int s0 = 0; s0 < parts; s0 += kTeams) {
+    const float ws = __shfl_sync(0xffffffffu, w, s0 + team, kLanes);
+    if (ws == 0.f) continue;                          // with no weight: what stands there may be no number
+    const float4* x = reinterpret_cast<const float4*>(scratch.o + (at0 + (int64_t)(s0 + team) * 2 * kTileRows) * D);
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      const float4 x = reinterpret_cast<const float4*>(scratch.o + at * D)[8 * k + lane8];
-      if (lse == -INFINITY) continue;                 // what stands there is no number
-      o[k].x = fmaf(w, x.x, o[k].x);
-      o[k].y = fmaf(w, x.y, o[k].y);
-      o[k].z = fmaf(w, x.z, o[k].z);
-      o[k].w = fmaf(w, x.w, o[k].w);
+      const float4 v = x[8 * k + lane8];
+      o[k].x = fmaf(ws, v.x, o[k].x);
+      o[k].y = fmaf(ws, v.y, o[k].y);
+      o[k].z = fmaf(ws, v.z, o[k].z);
+      o[k].w = fmaf(ws, v.w, o[k].w);
     }
   }
   const int t = (int)row / p.group, head = blockIdx.x % p.h_kv, hq = head * p.group + (int)row - t * p.group;
   const int64_t to = (int64_t)(ma.y + t) * p.h_q + hq;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  auto all = [](float v) {                            // over the teams
+#pragma unroll
+    for (int off = 8; off < kLanes; off *= 2) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  };
 #pragma unroll
   for (int k = 0; k < kV; ++k) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(o[k].x * inv, o[k].y * inv);
-    __nv_bfloat162 b = __floats2bfloat162_rn(o[k].z * inv, o[k].w * inv);
-    reinterpret_cast<uint2*>(p.o + to * D)[8 * k + lane8] =
-        make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+    __nv_bfloat162 a = __floats2bfloat162_rn(all(o[k].x) * inv, all(o[k].y) * inv);
+    __nv_bfloat162 b = __floats2bfloat162_rn(all(o[k].z) * inv, all(o[k].w) * inv);
+    if (team == 0 && row < ma.w)
+      reinterpret_cast<uint2*>(p.o + to * D)[8 * k + lane8] =
+          make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
   }
-  if (lane8 == 0) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  if (lane == 0 && row < ma.w) p.lse[to] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 namespace {
@@ -811,12 +832,13 @@ cudaError_t launch_as(const Q8Params& p, int64_t rows, const Q8Scratch& scratch,
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(items * p.h_kv), 2 * kTileRows / kJoinRows);
-  cfg.blockDim = dim3(8 * kJoinRows);
+  const int teams = splits <= 8 ? 1 : 4;
+  cfg.gridDim = dim3((unsigned)(items * p.h_kv), 2 * kTileRows * 8 * teams / kJoinThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q8_join_kernel<D>, p, scratch, splits);
+  return cudaLaunchKernelEx(&cfg, teams == 1 ? q8_join_kernel<D, 1> : q8_join_kernel<D, 4>, p, scratch, splits);
 }
 
 template <int D, bool kInt8>
