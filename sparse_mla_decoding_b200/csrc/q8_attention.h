@@ -29,18 +29,18 @@ constexpr int kQ8SpanTokens = 16;
 // decode kernel, and so few tiles that they are over before a CTA of the other is.
 // Measured, decode against tensor cores, us, 32 heads over 8, d = 128:
 //   rows of a request      16          32          48          64         128
-//   32 of 4096 tokens   62 / 123   101 / 123   143 / 123   183 / 124
-//   4 of 8192           29 / 42     41 / 42     53 / 42     64 / 42    110 / 43
-//   1 of 60000          39 / 68     58 / 68     76 / 69     92 / 68    162 / 69
-//   1 of 8192           17 / 26     21 / 26     25 / 26     26 / 26     36 / 26
-//   1 of 8192, 1 head   15 / 30     15 / 30     15 / 31     15 / 30     17 / 30
+//   32 of 4096 tokens   62 / 123   101 / 124   143 / 124   183 / 125
+//   4 of 8192           29 / 38     41 / 38     53 / 39     64 / 39    110 / 47
+//   1 of 60000          39 / 61     58 / 61     76 / 61     92 / 62    162 / 62
+//   1 of 8192           17 / 20     21 / 20     25 / 20     26 / 21     36 / 21
+//   1 of 8192, 1 head   15 / 18     15 / 18     15 / 18     15 / 18     17 / 18
 inline bool q8_decode_pays(int64_t batch, int64_t h_kv, int64_t group, int64_t total_q, int64_t max_q, bool docs,
                            int sms) {
   if (max_q > total_q || (docs && max_q > kQ8SpanTokens)) return false;
   const auto tiles = [&](int64_t rows) {              // at most, of one head
     return std::min(batch * ((max_q * group + rows - 1) / rows), total_q * group / rows + batch);
   };
-  return tiles(16) <= 2 * tiles(256) || 6 * tiles(16) * h_kv <= sms;
+  return tiles(16) <= 2 * tiles(256) || 16 * tiles(16) * h_kv <= sms;
 }
 
 // Partials of the decode kernel: two slots of kQ8PartRows rows for each warp and for
