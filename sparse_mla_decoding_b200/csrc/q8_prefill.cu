@@ -42,7 +42,8 @@
 // pipe).  A step takes 1900 (long loops) to 2300 clocks: the chain of a softmax warp
 // from S to P is longer than the products of the other tile.  A CTA takes about 8 us
 // beside its steps (finding its request, Q, the output), which is what short prompts
-// and documents wait for.  8192 tokens on 8192, 32 heads: 1.46 ms, 1.13 PFLOP/s.
+// and documents wait for.  8192 tokens on 8192, 32 heads: 1.46 ms, 1.13 PFLOP/s
+// (1.6 ms where the power cap lowers the clocks).
 #include <cuda_runtime.h>
 
 #include <algorithm>
