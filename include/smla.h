@@ -472,8 +472,10 @@ size_t smla_gqa_workspace_bytes(int head_dim, int device);
  * whose block lies outside the table or the cache is skipped and flagged; so is
  * a request whose token offsets run backwards or past total_q (other requests
  * of such a call may be skipped with it).  What the cache holds behind a
- * request's length never reaches a result; a NaN in a value row within it
- * reaches every token of the request that shares a tile with one that sees it.
+ * request's length never reaches a result.  A NaN in a key row within it makes
+ * o and lse NaN for the tokens that see it, and for no others; a NaN in a value
+ * row reaches o of every token of the request that shares a tile with one that
+ * sees it.
  */
 int smla_gqa_attention_with_kvcache(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t total_q,
                                     int h_q, const smla_q8_cache* cache, const int32_t* block_table, int max_blocks,

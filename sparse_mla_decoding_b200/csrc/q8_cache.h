@@ -170,6 +170,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// The same, NaN where one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // x_j = cap tanh(x_j fc) of N scores; a vote of the warp over the N picks the way.
 // All |y| = |x fc| <= 0.35: y P(y^2), P a degree-3 fit to tanh(y)/y in relative error

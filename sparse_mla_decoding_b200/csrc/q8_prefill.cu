@@ -240,7 +240,7 @@ constexpr int kRowLanes = D / 8;          // lanes that read or write a row of q
 // exponentials that the special function units would be waited for: n = round(x)
 // by adding 1.5 * 2^23, 2^(x - n) by a degree-4 fit in relative error (2.7e-6 at
 // most, 4e-8 in the mean; reweighted least squares on Chebyshev nodes), n added to
-// the exponent field.  Below 2^-126: 2^-126.
+// the exponent field.  Below 2^-126, and for NaN: 2^-126.
 __device__ __forceinline__ float2 ex2_poly(float2 x) {
   x.x = fmaxf(x.x, -126.f);
   x.y = fmaxf(x.y, -126.f);
@@ -470,8 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
 #pragma unroll
         for (int j = 0; j < 64; j += 8)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top[k] = max3(top[k], S[j + 2 * k], S[j + 2 * k + 1]);
-        const float peak = fmaf(max3(top[0], top[1], fmaxf(top[2], top[3])), f, bs.rel);   // f > 0
+          for (int k = 0; k < 4; ++k) top[k] = max3_nan(top[k], S[j + 2 * k], S[j + 2 * k + 1]);
+        const float peak = fmaf(max3_nan(top[0], top[1], max3_nan(top[2], top[3], top[3])), f, bs.rel);   // f > 0
+        // a NaN score makes the row NaN, and so does an infinite one (inf - inf): by the sum,
+        // as ex2_poly keeps neither
+        if (!(peak < INFINITY)) l = __int_as_float(0x7FFFFFFF);
         if (__any_sync(0xffffffffu, peak > m + 8.f)) {
           const float now = fmaxf(m, peak);
           const float a = now == -INFINITY ? 1.f : ex2(m - now);

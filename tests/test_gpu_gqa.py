@@ -194,6 +194,30 @@ def test_far_query_sizes(size):
     check(x, softmax_scale=float(0.125 / size))
 
 
+@pytest.mark.parametrize("hint", [1, LONG])
+@pytest.mark.parametrize("mods", ["", "cap", "slopes", "alone"])
+def test_a_nan_key_reaches_every_row_that_sees_it(mods, hint):
+    """At each place among eight neighbours, and as the only key that a row sees; other rows and heads are as ever."""
+    kw = {"max_seqlen_q": hint}
+    if mods == "cap":
+        kw["softcap"] = 30.0
+    if mods == "slopes":
+        kw["alibi_slopes"] = np.full(8, 0.05, np.float32)
+    for at in range(176, 184):
+        x = build([40, 1], [200, 190], 8, 2, 128 if at % 2 else 64, "e4m3", 1900 + at)
+        if mods == "alone":
+            kw["doc_bounds"] = np.array([(0, 200)] * 39 + [(at, at + 1)] + [(at, at + 1)], np.int32)
+        for r in range(2):
+            x["kc"].view(torch.int8)[x["table"][r, at // 64], 0, at % 64, 11] = 127
+        o, lse, (status, _) = call(x, **kw)
+        assert status == 0
+        sees = np.zeros((41, 8), bool)
+        sees[at - 160:, :4] = True                    # tokens at positions 160 .. 199, and the other request's
+        hit = torch.from_numpy(sees)
+        assert torch.isnan(o.cpu()[hit]).all() and torch.isnan(lse.cpu()[hit]).all()
+        U.compare(o, lse, reference(x, **kw), rows=~sees)
+
+
 def test_strided_queries_scales_and_blocks():
     """Query rows inside a fused projection; keys and values in one allocation."""
     import sparse_mla_decoding_b200 as smla
