@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
         const int t = token_of(e.rt, in_tile, hh), hq = e.head * p.group + hh;
         if (t >= x.n) continue;
         // rows g and g + 8 of output tile k: d = kCols g + 2k and + 1
-        if (whole) {
+        if (whole) {                                  // no visible key: 0, though a NaN value may be in O
           const int64_t at = (int64_t)(x.q0 + t) * p.h_q + hq;
           uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + kCols * g);
 #pragma unroll
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               __nv_bfloat162 b = __floats2bfloat162_rn(O[nt][4 * k + j][i] * inv, O[nt][4 * k + j][2 + i] * inv);
-              u[j] = *reinterpret_cast<uint32_t*>(&b);
+              u[j] = s == 0.f ? 0u : *reinterpret_cast<uint32_t*>(&b);
             }
             dst[k] = make_uint4(u[0], u[1], u[2], u[3]);
           }

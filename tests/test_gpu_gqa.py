@@ -218,6 +218,18 @@ def test_a_nan_key_reaches_every_row_that_sees_it(mods, hint):
         U.compare(o, lse, reference(x, **kw), rows=~sees)
 
 
+@pytest.mark.parametrize("hint", [1, LONG])
+@pytest.mark.parametrize("length", [50, 190])
+def test_a_token_that_sees_nothing_beside_nan_values(length, hint):
+    x = build([2, 2], [length, length + 1], 8, 2, 128, "e4m3", 1950)
+    x["vc"].view(torch.int8)[x["table"][:, 0], :, 3] = 127
+    docs = np.array([(5, 5), (0, 1000)] * 2, np.int32)
+    o, lse, (status, _) = call(x, doc_bounds=docs, max_seqlen_q=hint)
+    assert status == 0
+    assert (o[::2] == 0).all() and torch.isneginf(lse[::2]).all()
+    assert torch.isnan(o[1::2]).all() and torch.isfinite(lse[1::2]).all()
+
+
 def test_strided_queries_scales_and_blocks():
     """Query rows inside a fused projection; keys and values in one allocation."""
     import sparse_mla_decoding_b200 as smla
