@@ -19,6 +19,7 @@ namespace smla {
 constexpr int kBlk = 64;          // tokens per cache block
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMostFactor = 3e38f;   // of a score: finite, so that a product of 0 stays 0
 
 // Everything an attention call over the cache needs; offsets and strides in
 // elements unless they say bytes.
@@ -183,14 +184,15 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // their relative precision and no special function is used; fc and cap go into the
 // coefficients, so a score costs 2.5 packed instructions.  Else 1 - 2 / (1 + exp(2
 // |y|)) with the sign of x, off by some 1e-7 of the cap.  (x is a product of f16
-// values, below 2^18, so x^2 stays in range.)
+// values, below 2^18, so x^2 stays in range; fc <= 2^9 keeps fc^7 cap, with caps up
+// to 2^60, inside fp32, and a finite factor keeps 0 at 0.)
 template <int N>
 __device__ __forceinline__ void cap_scores(float* x, float fc, float cap) {
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < N; j += 2) top = max3(top, fabsf(x[j]), fabsf(x[j + 1]));
-  if (__any_sync(0xffffffffu, !(top * fc <= 0.35f))) {
-    const float fe = fc * (2.f * kLog2e);
+  if (__any_sync(0xffffffffu, !(top * fc <= 0.35f && fc <= 512.f))) {
+    const float fe = fminf(fc * (2.f * kLog2e), kMostFactor);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       float r;

@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = row_fac[nt][i] * e.k_scale * sl2;
+          const float f = fminf(row_fac[nt][i] * e.k_scale * sl2, kMostFactor);
           if (p.cap > 0.f) {
             float x[8];
 #pragma unroll

@@ -435,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         const BlockScales bs = sm.scales[i % kScaleRing];
         const int j0 = (first + i) * kBlk;
         // never 0: a masked score is -inf and has to stay so
-        float f = fmaxf(fs * bs.k, 1e-30f);
+        float f = fminf(fmaxf(fs * bs.k, 1e-30f), kMostFactor);
         tmem_wait_ld();
         // capped and biased scores in place (f then is 1)
         if constexpr (kMods) {
           if (p.cap > 0.f) {
-            cap_scores<64>(S, fs * bs.k * p.inv_cap_log2, p.cap_log2);
+            cap_scores<64>(S, f * p.inv_cap_log2, p.cap_log2);
             f = 1.f;
           }
           if (p.slopes) {

@@ -230,6 +230,19 @@ def test_a_token_that_sees_nothing_beside_nan_values(length, hint):
     assert torch.isnan(o[1::2]).all() and torch.isfinite(lse[1::2]).all()
 
 
+@pytest.mark.parametrize("mods", ["cap", "cap+slopes", "slopes", ""])
+@pytest.mark.parametrize("n", [1, 40])
+def test_zero_scores_under_extreme_scales(n, mods):
+    """All scores are 0 whatever they are multiplied by: o is the mean of the values."""
+    x = build([n], [150], 8, 2, 64, "int8", 1960, poison=False)
+    x["kc"].zero_()
+    x["ks"].fill_(1.0)
+    x["k"] = np.zeros_like(x["k"])
+    kw = {"alibi_slopes": np.full(8, 0.01, np.float32)} if "slopes" in mods else {}
+    for scale, cap in [(1e6, 1.0), (1e38, 1.0), (1e38, 2.0 ** -60), (1e30, 2.0 ** 60)]:
+        check(x, softmax_scale=scale, **({"softcap": cap} if "cap" in mods else {}), **kw)
+
+
 def test_strided_queries_scales_and_blocks():
     """Query rows inside a fused projection; keys and values in one allocation."""
     import sparse_mla_decoding_b200 as smla
