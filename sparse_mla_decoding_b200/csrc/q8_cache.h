@@ -213,6 +213,12 @@ __device__ __forceinline__ void cap_scores(float* x, float fc, float cap) {
   }
 }
 
+// The softmax reference m of a row lies kHead below its running maximum, so P = 2^(x - m)
+// is 2^kHead there and, as m is raised only once the maximum is kHead + kLag above it, at
+// most 2^15, inside f16.  f16 drops what is below 2^-25: keys of 2^-32 of the largest
+// probability, of which a million weigh 2^-12, less than o's own rounding.
+constexpr float kHead = 7.f, kLag = 8.f;
+
 // log2 of a value scale relative to `base`, kept within 2^+-60 (a zero scale
 // has only zero codes behind it, so any value does; the clamp keeps the
 // softmax denominator inside fp32).

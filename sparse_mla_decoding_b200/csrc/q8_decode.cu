@@ -27,7 +27,8 @@
 // the exponent,
 //   p_j = 2^(x_j + log2 v_scale - m),
 // so one accumulator holds blocks of different scales; the sum of the softmax
-// takes the factor out again per block.  P is rounded to f16 once (2^-11).
+// takes the factor out again per block.  P is rounded to f16 once (2^-11), with m 7 to
+// 15 below the row's largest exponent.
 //
 // Bound by HBM: d + 1/16 bytes a key, value and head; what has to keep up is the
 // conversion, about 470 instructions a warp and block (16 KB at d = 128).  What costs
@@ -672,15 +673,14 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 8));
           top[nt][i] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 16)) + rel;
-          grew |= top[nt][i] > m[nt][i] + 8.f;
+          grew |= top[nt][i] > m[nt][i] + (kHead + kLag);
         }
-      // P may grow to 2^8 before the accumulators are rescaled (f16 reaches 2^15)
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float now = fmaxf(m[nt][i], top[nt][i]);
+            const float now = fmaxf(m[nt][i], top[nt][i] - kHead);
             const float a = now == -INFINITY ? 1.f : ex2(m[nt][i] - now);
             m[nt][i] = now;
             l[nt][i] *= a;

@@ -8,7 +8,7 @@
 // 16 warps:
 //   0-3, 4-7  softmax of row tile 0 and 1; thread = row.  A thread reads its
 //             row of S from TMEM, writes P (f16) over it and, when its maximum
-//             grows by more than 2^8, rescales its row of O in TMEM.  Before
+//             has grown by 2^8, rescales its row of O in TMEM.  Before
 //             that the eight warps bring Q in.
 //   8-11      producers: codes from global memory to registers (two blocks
 //             ahead), to f16, to 128-byte-swizzled shared memory.
@@ -475,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         // a NaN score makes the row NaN, and so does an infinite one (inf - inf): by the sum,
         // as ex2_poly keeps neither
         if (!(peak < INFINITY)) l = __int_as_float(0x7FFFFFFF);
-        if (__any_sync(0xffffffffu, peak > m + 8.f)) {
-          const float now = fmaxf(m, peak);
+        if (__any_sync(0xffffffffu, peak > m + (kHead + kLag))) {
+          const float now = fmaxf(m, peak - kHead);
           const float a = now == -INFINITY ? 1.f : ex2(m - now);
           m = now;
           l *= a;

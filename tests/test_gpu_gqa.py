@@ -243,6 +243,30 @@ def test_zero_scores_under_extreme_scales(n, mods):
         check(x, softmax_scale=scale, **({"softcap": cap} if "cap" in mods else {}), **kw)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [1, 40])
+def test_small_probabilities_beside_a_large_one_reach_the_output(n, kind):
+    """Each block's first key has e^18 = 2^25.97 times the weight of each other, and value 0:
+    o = w / (1 + w) of the others' weight w.  P is at least 2^7 at the running maximum, so the
+    others' are 2^-18.97 or more, where f16 is off by at most 2^-25, 2^-6.03 of it; with the
+    half step of o 2^-8 and 2^-10 for all else."""
+    x = build([n], [290], 4, 1, 64, kind, 1970, poison=False)
+    for c in ("kc", "vc"):
+        x[c].copy_(torch.zeros(x[c].shape).to(x[c].dtype))
+    x["kc"][:, :, 0, 0] = 18.0 if kind == "e4m3" else 18
+    x["vc"][:, :, 1:] = 1.0 if kind == "e4m3" else 1
+    x["ks"].fill_(1.0)
+    x["vs"].fill_(1.0)
+    x["k"], x["v"] = x["kc"].double().numpy(), x["vc"].double().numpy()
+    x["q"].zero_()
+    x["q"][:, :, 0] = 1.0
+    ref = U.attention(x["q"].double().numpy(), x["k"], x["v"], x["table"], x["lens"], x["cu"], scale=1.0,
+                      v_scale=x["vs"].double().numpy())[0]
+    for hint in (1, LONG):
+        o = call(x, softmax_scale=1.0, max_seqlen_q=hint)[0].double().cpu().numpy()
+        assert (np.abs(o - ref) <= (2.0 ** -6.03 + 2.0 ** -8 + 2.0 ** -10) * ref).all()
+
+
 def test_strided_queries_scales_and_blocks():
     """Query rows inside a fused projection; keys and values in one allocation."""
     import sparse_mla_decoding_b200 as smla
