@@ -540,15 +540,17 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
           m[nt][i] = -INFINITY;
           l[nt][i] = 0.f;
           int lo = 0, hi = 0x7FFFFFFF;
+          float2 bias = make_float2(0.f, 0.f);      // an absent row's scores are 0, and its vote always the same
           if (t < x.n) {
             q8_visible(p, x, t, lo, hi);
-            if (p.slopes && g == 0)
-              sm.bias[warp][8 * nt + 2 * c + i] =
-                  make_float2((float)(x.len - x.n + t), p.slopes[head * p.group + hh] * kLog2e);
+            if (p.slopes) bias = make_float2((float)(x.len - x.n + t), p.slopes[head * p.group + hh] * kLog2e);
             all_lo = max(all_lo, lo);
             all_hi = min(all_hi, hi);
           }
-          if (g == 0) sm.sees[warp][8 * nt + 2 * c + i] = make_int2(lo, hi);
+          if (g == 0) {
+            sm.sees[warp][8 * nt + 2 * c + i] = make_int2(lo, hi);
+            sm.bias[warp][8 * nt + 2 * c + i] = bias;
+          }
         }
 #pragma unroll
         for (int t = 0; t < kOut; ++t)

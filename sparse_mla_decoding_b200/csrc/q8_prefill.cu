@@ -370,6 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     // This thread's row: token, query head, and which positions it sees.
     int lo = 0, hi = 0x7FFFFFFF;
     int64_t q_at = -1;                                // in q; -1: no row
+    // an absent row has no bias either: its scores are 0, and its vote is always the same
+    if (kMods && p.slopes) sm.bias[tid] = make_float2(0.f, 0.f);
     if (row0 + tid < rows_all) {
       const int t = (int)(row0 + tid) / p.group, hq = head * p.group + (int)(row0 + tid) - t * p.group;
       q8_visible(p, x, t, lo, hi);

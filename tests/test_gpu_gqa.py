@@ -431,6 +431,23 @@ def test_repeated_calls_are_bitwise_equal():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h_q,h_kv,n", [(2, 2, 1), (12, 4, 1), (4, 4, 3), (4, 4, 33)])
+def test_biased_calls_do_not_depend_on_the_calls_before(h_q, h_kv, n, d):
+    """Row tiles with absent rows, behind calls that leave other slopes in shared memory."""
+    x = build([n] * 3, [3000, 900, 400], h_q, h_kv, d, "int8", 1980 + d)
+    slopes = np.exp2(-np.arange(h_q, dtype=np.float32))
+    others = [(build([1] * 64, [2000] * 64, 8, 1, d, "int8", 1985), 1), (build([2] * 64, [2000] * 64, 8, 1, d, "int8", 1986), 2),
+              (build([64] * 40, [200] * 40, 16, 4, d, "int8", 1987), LONG)]
+    for hint in (1, LONG):
+        seen = []
+        for slope in (0.0, -1.0, -100.0, 0.0):
+            for other, h in others:
+                call(other, alibi_slopes=np.full(other["q"].shape[1], slope, np.float32), max_seqlen_q=h)
+            seen.append(call(x, alibi_slopes=slopes, max_seqlen_q=hint))
+        assert all(torch.equal(seen[0][0], s[0]) and torch.equal(seen[0][1], s[1]) for s in seen)
+
+
 @pytest.mark.parametrize("hint", [1, LONG])
 def test_a_captured_call_replays_on_new_inputs(hint):
     """A graph keeps its own scratch: replays beside eager calls, on another stream, give the eager results."""
