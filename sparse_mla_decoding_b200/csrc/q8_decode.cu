@@ -632,6 +632,15 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
       }
       const float rel = rel_log2(e.v_scale, base_log2), unrel = ex2(-rel);
       const bool edge = j0 < all_lo || j0 + kBlk > all_hi;
+      if (p.cap > 0.f && sm.request[warp][e.request].x.len - j0 < kBlk) {
+        // what stands behind the length has no vote on the cap's form
+        const int tail = sm.request[warp][e.request].x.len - j0 - g;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (8 * j >= tail) S[nt][j >> 1][2 * (j & 1)] = S[nt][j >> 1][2 * (j & 1) + 1] = 0.f;
+      }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll

@@ -448,6 +448,21 @@ def test_biased_calls_do_not_depend_on_the_calls_before(h_q, h_kv, n, d):
         assert all(torch.equal(seen[0][0], s[0]) and torch.equal(seen[0][1], s[1]) for s in seen)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hint", [1, LONG])
+def test_capped_scores_do_not_depend_on_what_stands_behind_the_length(hint, kind):
+    """Scores of a few hundredths of the cap; the rows behind hold codes whose scores reach it."""
+    x = build([1, 1, 3], [40, 100, 191], 8, 2, 128, kind, 1990, poison=False)
+    clean = call(x, softcap=30.0, max_seqlen_q=hint)
+    for r, n in enumerate(x["lens"]):
+        b, row = x["table"][r, n // 64], n % 64
+        for h in range(2):
+            s = torch.sign(x["q"][x["cu"][r], 4 * h].float())
+            x["kc"][b, h, row:] = (s * (448 if kind == "e4m3" else 127)).to(x["kc"].dtype)
+    dirty = call(x, softcap=30.0, max_seqlen_q=hint)
+    assert torch.equal(clean[0], dirty[0]) and torch.equal(clean[1], dirty[1])
+
+
 @pytest.mark.parametrize("hint", [1, LONG])
 def test_a_captured_call_replays_on_new_inputs(hint):
     """A graph keeps its own scratch: replays beside eager calls, on another stream, give the eager results."""
