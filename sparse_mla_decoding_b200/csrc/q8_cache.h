@@ -72,7 +72,8 @@ __device__ __forceinline__ Q8Request q8_request(const Q8Params& p, int r, bool* 
   return x;
 }
 
-// The cache positions [lo, hi) that new token t of a request sees.
+// The cache positions [lo, hi) that new token t of a request sees, both >= 0: the kernels
+// take positions off them.
 __device__ __forceinline__ void q8_visible(const Q8Params& p, const Q8Request& x, int t, int& lo, int& hi) {
   lo = 0;
   hi = x.len;
@@ -82,6 +83,7 @@ __device__ __forceinline__ void q8_visible(const Q8Params& p, const Q8Request& x
     lo = max(d.x, 0);
     hi = min(hi, d.y);
   }
+  hi = max(hi, 0);
 }
 
 // ---------------------------------------------------------------------------

@@ -126,6 +126,14 @@ def test_documents(d, causal):
     assert torch.isinf(lse[-1]).all() and (o[-1] == 0).all()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_documents_that_end_far_below_zero(causal):
+    lo, hi = -(1 << 31), (1 << 31) - 1
+    x = build([6, 50], [300, 310], 8, 2, 64, "int8", 2000)
+    docs = [(0, 300), (0, lo), (hi, lo), (lo, lo), (hi, hi), (lo, hi)] + [(0, 310), (0, lo), (hi, lo), (7, -5), (lo, hi)] * 10
+    check(x, doc_bounds=np.array(docs, np.int32), causal=causal)
+
+
 def test_prefix_and_documents_and_bias_together():
     x = build([40, 3], [200, 90], 6, 2, 128, "e4m3", 550)
     docs = np.array([(0, 180)] * 20 + [(180, 200)] * 20 + [(10, 90)] * 3, np.int32)
