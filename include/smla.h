@@ -367,8 +367,9 @@ typedef struct {
  *   entry ceil(len / 64) + i = free_blocks[num_free - 1 - (blocks of the
  *                              requests before r) - i].
  * A request fits if its blocks are covered by num_free, its row has room for
- * them and its tokens end within max_new_tokens; one that does not keeps its
- * length and its table row, and its tokens get slots -1.
+ * them, its length stays below 2^31 and its tokens end within max_new_tokens;
+ * one that does not keeps its length and its table row, and its tokens get
+ * slots -1.
  *   block_table   : device int32 [batch][max_blocks], fresh entries written
  *   cache_seqlens : device int32 [batch], before the new tokens
  *   new_lens      : device int32 [batch]

@@ -6,7 +6,8 @@
 //   first_r  = sum_{i < r} need_i,   cu_r = sum_{i < r} new_i
 //   block ceil(len_r / 64) + i of request r = free[num_free - 1 - first_r - i]
 //   slot of its token t: block of position len_r + t, times 64, plus the rest.
-// A request whose blocks do not all fit keeps its length and gets slots -1.
+// A request whose blocks do not all fit keeps its length and gets slots -1; so does one
+// whose length would pass 2^31 - 1.
 //
 // Bound by latency: the smallest step reads and writes a few KB.  Every CTA
 // scans the lengths itself (one shuffle scan of tokens and blocks per 1024
@@ -23,6 +24,9 @@
 namespace smla {
 
 constexpr int kTableThreads = 1024;
+
+// Blocks of len tokens, 0 <= len < 2^31.
+__device__ __forceinline__ int blocks_of(int len) { return (int)(((uint32_t)len + 63u) / 64u); }
 
 __global__ void __launch_bounds__(kTableThreads)
     extend_block_table_kernel(int32_t* block_table, int max_blocks, const int32_t* __restrict__ seqlens,
@@ -48,8 +52,9 @@ __global__ void __launch_bounds__(kTableThreads)
     if (r < batch) {
       len = max(seqlens[r], 0);
       fresh = max(new_lens[r], 0);
-      const int64_t after = ((int64_t)len + fresh + 63) / 64;
-      need = after <= max_blocks ? (int)(after - ((int64_t)len + 63) / 64) : -1;
+      const int64_t sum = (int64_t)len + fresh;
+      const bool room = sum <= 0x7FFFFFFF && (sum + 63) / 64 <= max_blocks;
+      need = room ? blocks_of((int)sum) - blocks_of(len) : -1;
     }
     uint64_t t64 = (uint64_t)fresh, b64 = (uint64_t)max(need, 0);   // inclusive sums of tokens and blocks
 #pragma unroll
@@ -94,7 +99,7 @@ __global__ void __launch_bounds__(kTableThreads)
     // table entries: a warp per request, the requests spread over the CTAs
     const int in_chunk = min(batch - r0, kTableThreads);
     for (int q = warp * gridDim.x + blockIdx.x; q < in_chunk; q += 32 * gridDim.x) {
-      const int n = s_need[q], at = (s_len[q] + 63) / 64;
+      const int n = s_need[q], at = blocks_of(s_len[q]);
       for (int i = lane; i < n; i += 32)
         block_table[(int64_t)(r0 + q) * max_blocks + at + i] = free_blocks[have - 1 - s_first[q] - i];
     }
@@ -110,7 +115,7 @@ __global__ void __launch_bounds__(kTableThreads)
       int64_t slot = -1;
       if (s_need[a] >= 0) {
         const int64_t pos = s_len[a] + (i - s_cu[a]);
-        const int blk = (int)(pos / 64), old = (s_len[a] + 63) / 64;
+        const int blk = (int)(pos / 64), old = blocks_of(s_len[a]);
         const int32_t id = blk < old ? block_table[(int64_t)(r0 + a) * max_blocks + blk]
                                      : free_blocks[have - 1 - s_first[a] - (blk - old)];
         slot = (int64_t)id * 64 + pos % 64;

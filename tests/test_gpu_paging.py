@@ -63,6 +63,35 @@ def test_requests_that_do_not_fit():
     tables([10, 5], [-3, 4], np.arange(5))
 
 
+def test_lengths_at_the_end_of_32_bits():
+    """A row of 2^25 + 1 blocks: tokens up to position 2^31 - 2 get their rows, in the last block
+    held or in a fresh one, and a length of 2^31 is declined."""
+    import sparse_mla_decoding_b200 as smla
+    top = 1 << 31
+    cols = (1 << 25) + 1
+    table = torch.full((1, cols), -1, dtype=torch.int32, device="cuda")
+    table[0, (1 << 25) - 2:(1 << 25)] = torch.tensor([500, 600], dtype=torch.int32)
+    table[0, (1 << 25) - 1:] = torch.tensor([600, -1], dtype=torch.int32)
+    free = torch.tensor([7, 8], dtype=torch.int32, device="cuda")
+    for length, new, fits in ((top - 63, 10, True), (top - 63, 62, True), (top - 70, 3, True), (top - 64, 63, True),
+                              (top - 63, 63, False), (top - 5, 10, False), (top - 1, 70, False), (top - 1, 0, True)):
+        t = table.clone()
+        args = [torch.tensor([a], dtype=torch.int32, device="cuda") for a in (length, new, 2)]
+        slots, cu, out, left = smla.extend_block_table(t, args[0], args[1], free, args[2], 70)
+        held = -(-length // BLOCK)                    # the entries before this one are the request's
+        need = -(-(length + new) // BLOCK) - held if fits else 0
+        want = [-1] * 70
+        if fits:
+            pages = {(1 << 25) - 2: 500, (1 << 25) - 1: 600 if held == 1 << 25 else 8}
+            want[:new] = [pages[p // BLOCK] * BLOCK + p % BLOCK for p in range(length, length + new)]
+        assert slots.tolist() == want
+        assert cu.tolist() == [0, new] and int(out) == length + (new if fits else 0) and int(left) == 2 - need
+        ref = table[0, -3:].tolist()
+        if need:
+            ref[held - (cols - 3)] = 8
+        assert t[0, -3:].tolist() == ref and torch.equal(t[0, :-3], table[0, :-3])
+
+
 def test_empty_batches():
     tables(np.zeros(0), np.zeros(0), np.arange(3), cols=1)
     tables(np.zeros(0), np.zeros(0), np.arange(3), cols=1, max_new=70)
