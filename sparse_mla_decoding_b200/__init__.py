@@ -809,8 +809,9 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     rc = _on_device(
         index, lib().smla_gqa_attention_with_kvcache, rows.data_ptr(), q_tok, q_head, total, h_q,
         ctypes.byref(cache), block_table.data_ptr(), cols, b, cache_seqlens.data_ptr(), cu, s_q,
-        total if max_seqlen_q is None else int(max_seqlen_q), 1 if causal else 0, scale, softcap, _ptr(alibi_slopes),
-        _ptr(prefix_lens), _ptr(doc_bounds), o.data_ptr(), lse.data_ptr(), at, room, _ptr(word), _raw_stream(index))
+        total if max_seqlen_q is None else min(int(max_seqlen_q), 0x7FFFFFFF), 1 if causal else 0, scale, softcap,
+        _ptr(alibi_slopes), _ptr(prefix_lens), _ptr(doc_bounds), o.data_ptr(), lse.data_ptr(), at, room, _ptr(word),
+        _raw_stream(index))
     if rc:
         _check(rc, "smla_gqa_attention_with_kvcache")
     if check_device_status and word is not None:

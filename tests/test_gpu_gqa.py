@@ -180,6 +180,12 @@ def test_hint_changes_nothing_that_is_computed(hint):
     check(x, max_seqlen_q=hint)
 
 
+@pytest.mark.parametrize("hint", [1 << 31, 1 << 40])
+def test_hints_of_any_size(hint):
+    x = build([1, 30], [100, 90], 8, 2, 128, "e4m3", 2010)
+    check(x, max_seqlen_q=hint)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_zero_scales_and_large_spreads(n):
     """Blocks of zero keys or values beside ordinary ones, and scales far apart."""
