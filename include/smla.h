@@ -341,7 +341,8 @@ int smla_flash_mla_with_kvcache_static_scratch(const void* q, const uint8_t* kvc
  * values, for instance); within a block the codes are dense.
  *   k_cache, v_cache : device, 16-byte aligned
  *   k_scale, v_scale : device float32 [num_blocks][h_kv]; finite, >= 0, those
- *                      of one request and head within 2^60 of one another
+ *                      above 0 of one request and head within 2^60 of one
+ *                      another
  *   *_block_stride   : bytes between blocks, a multiple of 16
  *   *_scale_stride   : floats between the scales of neighbouring blocks
  *   head_dim         : 64 or 128;  h_kv at most 65535, h_kv * head_dim * 64 < 2^31

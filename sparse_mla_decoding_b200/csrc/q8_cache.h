@@ -222,8 +222,8 @@ __device__ __forceinline__ void cap_scores(float* x, float fc, float cap) {
 constexpr float kHead = 7.f, kLag = 8.f;
 
 // log2 of a value scale relative to `base`, kept within 2^+-60 (a zero scale
-// has only zero codes behind it, so any value does; the clamp keeps the
-// softmax denominator inside fp32).
+// has only zero codes behind it, so any value does, and none is a base; the
+// clamp keeps the softmax denominator inside fp32).
 __device__ __forceinline__ float rel_log2(float scale, float base_log2) {
   return fminf(fmaxf(log2f(scale) - base_log2, -60.f), 60.f);
 }

@@ -442,8 +442,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
   // of rows 2c and 2c + 1 of each column block: power of two of q, softmax state
   float row_fac[NT][2], m[NT][2], l[NT][2];
   int all_lo = 0, all_hi = 0;                       // what every row of the tile sees
-  float base_log2 = 0.f;
-  bool opened = false;                              // base_log2 is set
+  float base_log2 = -INFINITY;                      // log2 of the unit's first value scale above 0
   const float sl2 = p.scale * kLog2e;
   // Token of row j of row tile rt, and its head in the group.  The division by the
   // group is by its inverse: exact below 2^20.
@@ -456,7 +455,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
 
   // The unit's result, or this warp's piece of it.
   auto close_unit = [&](const Entry& e, const Q8Request& x, bool whole, bool begun_here) {
-    const float back = ex2(base_log2);
+    const float back = exp2f(base_log2);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -465,7 +464,10 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
         s += __shfl_xor_sync(0xffffffffu, s, 4);
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
-        const float inv = s == 0.f ? 0.f : back / s;
+        // the scale apart from 1 / s: for values of 2^-100 their product would lose bits
+        const float inv = s == 0.f ? 0.f : 1.f / s;
+#pragma unroll
+        for (int k = 0; k < kOut; ++k) O[nt][k][i] *= inv, O[nt][k][2 + i] *= inv;
         const float lse2 = s == 0.f ? -INFINITY : m[nt][i] + log2f(s);
         const int in_tile = 8 * nt + 2 * c + i;
         int hh;
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
             uint32_t u[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              __nv_bfloat162 b = __floats2bfloat162_rn(O[nt][4 * k + j][i] * inv, O[nt][4 * k + j][2 + i] * inv);
+              __nv_bfloat162 b = __floats2bfloat162_rn(O[nt][4 * k + j][i] * back, O[nt][4 * k + j][2 + i] * back);
               u[j] = s == 0.f ? 0u : *reinterpret_cast<uint32_t*>(&b);
             }
             dst[k] = make_uint4(u[0], u[1], u[2], u[3]);
@@ -491,8 +493,8 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
           float4* dst = reinterpret_cast<float4*>(scratch.o + (slot * kPartRows + in_tile) * D + kCols * g);
 #pragma unroll
           for (int k = 0; k < kOut / 2; ++k)
-            dst[k] = make_float4(O[nt][2 * k][i] * inv, O[nt][2 * k][2 + i] * inv, O[nt][2 * k + 1][i] * inv,
-                                 O[nt][2 * k + 1][2 + i] * inv);
+            dst[k] = make_float4(O[nt][2 * k][i] * back, O[nt][2 * k][2 + i] * back, O[nt][2 * k + 1][i] * back,
+                                 O[nt][2 * k + 1][2 + i] * back);
           if (g == 0) scratch.lse[slot * kPartRows + in_tile] = lse2;
         }
       }
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
       const int head = ring[v % kRing].head, rt = ring[v % kRing].rt;
       const Q8Request x = sm.request[warp][ring[v % kRing].request].x;
       begun_here = ends & 1;
-      opened = false;
+      base_log2 = -INFINITY;
       all_lo = 0;
       all_hi = 0x7FFFFFFF;
       uint4 raw_q[NT][kPer / 8];                    // q of row 8 nt + g
@@ -626,10 +628,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
     // ---- softmax
     uint32_t P[NT][4][2];                           // [16 keys][keys 2c, 2c + 1 and + 8 of row g]
     if (e.block >= 0) {
-      if (!opened) {
-        base_log2 = e.v_scale > 0.f ? log2f(e.v_scale) : 0.f;
-        opened = true;
-      }
+      if (base_log2 == -INFINITY) base_log2 = log2f(e.v_scale);
       const float rel = rel_log2(e.v_scale, base_log2), unrel = ex2(-rel);
       const bool edge = j0 < all_lo || j0 + kBlk > all_hi;
       if (p.cap > 0.f && sm.request[warp][e.request].x.len - j0 < kBlk) {

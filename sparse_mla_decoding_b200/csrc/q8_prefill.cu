@@ -78,7 +78,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct BlockScales {
   float k;                                // key scale; negative where the block is not there
-  float rel, unrel;                       // log2 of the value scale over the first one's, and 2^-rel
+  float rel, unrel;                       // log2 of the value scale over the first one above 0, and 2^-rel
 };
 
 template <int D>
@@ -93,7 +93,7 @@ struct PrefillShared {                    // at a 1024-byte boundary
   uint64_t odone[2][2], qfull;
   uint32_t tmem;
   int lo, hi;                             // positions that any row sees
-  float base_log2;
+  float base;                             // the first value scale above 0, else 0
   Q8Request x;
   int64_t row0, rows_all;
   bool bad;                               // its offsets
@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         const int64_t row0 = v_sm.row0, rows_all = v_sm.rows_all;
         const int q0 = v_sm.x.q0, part = v_sm.part, head = blockIdx.y, lane = me & 31, warp = me >> 5;
         const bool none = m == -INFINITY && !(l != l);
-        const float inv = none ? 0.f : ex2(sm.base_log2) / l;
+        // the scale apart from 1 / l: for values of 2^-100 their product would lose bits
+        const float inv = none ? 0.f : 1.f / l, base = v_sm.base;
         const uint32_t qs = smem_u32(sm.q[warp >> 2]);
 #pragma unroll 2
         for (int c = 0; c < D; c += 32) {
@@ -548,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
             float4* dst = reinterpret_cast<float4*>(scratch.o + ((int64_t)part * 2 * kTileRows + me) * D + c);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+              dst[k] = make_float4(o[4 * k] * inv * base, o[4 * k + 1] * inv * base, o[4 * k + 2] * inv * base,
+                                   o[4 * k + 3] * inv * base);
             continue;
           }
 #pragma unroll
@@ -556,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
             uint32_t v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {             // O is not written where there are no blocks
-              __nv_bfloat162 b = __floats2bfloat162_rn(none ? 0.f : o[8 * k + 2 * j] * inv,
-                                                       none ? 0.f : o[8 * k + 2 * j + 1] * inv);
+              __nv_bfloat162 b = __floats2bfloat162_rn(none ? 0.f : o[8 * k + 2 * j] * inv * base,
+                                                       none ? 0.f : o[8 * k + 2 * j + 1] * inv * base);
               v[j] = *reinterpret_cast<uint32_t*>(&b);
             }
             sts128(qs + operand_at(me & 127, c / 8 + k), v[0], v[1], v[2], v[3]);
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     const int q = warp - 8, sub = lane >> 2, c4 = lane & 3;
     // Table entries and scales of 32 blocks, one a lane.
     int page = -1;
-    float kscale = -1.f, vscale = 0.f;
+    float kscale = -1.f, vscale = 0.f, base_log2 = -INFINITY;
     auto load_entries = [&](int b) {                  // block b: this lane's
       page = -1;
       kscale = -1.f;
@@ -610,11 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
           page = -1;
         }
       }
+      if (base_log2 == -INFINITY) {                   // no scale above 0 so far; blocks of zeros want no base
+        const uint32_t above = __ballot_sync(0xffffffffu, vscale > 0.f);
+        const float base = __shfl_sync(0xffffffffu, vscale, above ? __ffs(above) - 1 : 0);
+        base_log2 = log2f(base);
+        if (tid == 256) sm.base = base;
+      }
     };
     load_entries(lane);
-    const float v0 = __shfl_sync(0xffffffffu, vscale, 0);
-    const float base = v0 > 0.f ? log2f(v0) : 0.f;
-    if (tid == 256) sm.base_log2 = base;
     const int code_off = (head * kBlk + 16 * q + sub) * D + 16 * c4;
     auto load_tile = [&](uint4 (&codes)[kLoads], int i, const uint8_t* cache, int64_t stride, int pg) {
       // rows behind the request's length count as zero codes
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         const int st = i % kStages;
         BlockScales bs;
         bs.k = ks[e];
-        bs.rel = rel_log2(vs[e], base);
+        bs.rel = rel_log2(vs[e], base_log2);
         bs.unrel = ex2(-bs.rel);
         int pg = -1;
         const bool more = i + 2 < blocks;

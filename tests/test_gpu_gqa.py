@@ -200,6 +200,24 @@ def test_zero_scales_and_large_spreads(n):
     check(x)
 
 
+@pytest.mark.parametrize("size", [2.0 ** -112, 2.0 ** -100, 2.0 ** 100])
+@pytest.mark.parametrize("n", [1, 40])
+def test_zero_value_scales_before_far_ones(n, size):
+    """The first blocks hold zeros (scale 0), the others values far from 1.  bf16's steps below
+    2^-126 are 2^-133, so the rounding of o there is off by up to 2^-134 whatever its size."""
+    x = build([n], [900], 8, 2, 64, "int8", 2020, poison=False)
+    blocks = x["table"][0, :15]
+    x["vs"][blocks] *= size
+    x["vs"][blocks[[0, 1, 9]]] = 0
+    x["vc"][blocks[[0, 1, 9]]] = 0
+    x["v"] = x["vc"].double().numpy() * x["vs"].double().numpy()[:, :, None, None]
+    o_ref, lse_ref, tol, tol_lse = reference(x)
+    for hint in (None, 1, LONG):
+        o, lse, (status, _) = call(x, max_seqlen_q=hint)
+        assert status == 0
+        U.compare(o, lse, (o_ref, lse_ref, tol + 2.0 ** -134, tol_lse))
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e30])
 def test_far_query_sizes(size):
     """Queries far outside f16's range: scores of ordinary size come from the softmax scale."""
