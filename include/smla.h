@@ -403,8 +403,9 @@ int smla_extend_block_table(int32_t* block_table, int max_blocks, const int32_t*
  *          magnitude among the new values is <= 448 (e4m3) or 127 (int8); 0 if
  *          all are zero
  *   now  = max(s, was), stored
- *   code = x / now rounded to nearest even and saturated (all 0 for now = 0);
- *          NaN is stored as NaN (e4m3) or 0 (int8), infinities saturate
+ *   code = x / now rounded to nearest even and saturated (0 for now = 0, of
+ *          infinities too); NaN is stored as NaN (e4m3, for now = 0 too) or 0
+ *          (int8), other infinities saturate
  * and where now > was the older codes become round(code * (was / now)).
  * Rows behind the last token are left as they were.  No two requests of a call
  * may write to the same block.

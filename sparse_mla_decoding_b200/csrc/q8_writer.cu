@@ -5,7 +5,8 @@
 //   s    = the smallest power of two with max |x| / s <= 448 (e4m3) or 127 (int8)
 //          over the new tokens' finite values; 0 if they are all zero
 //   now  = max(s, was);  code = round-to-nearest-even(x / now), saturated
-//   older codes become round(code * (was / now)) where now > was.
+//   older codes become round(code * (was / now)) where now > was;
+// for now = 0 all codes are 0 but those of NaN, which e4m3 keeps at any scale.
 // Powers of two make x / s and the rescaling of e4m3 codes exact (up to the
 // code's own rounding), and a block that fills token by token is rescaled only
 // when its maximum crosses a power of two, not at every new maximum.
@@ -179,6 +180,17 @@ __global__ void __launch_bounds__(kThreads, 8) quantize_kv_blocks_kernel(const _
       for (int j = 0; j < 8; ++j) {
         const float v = __fdiv_rn(__bfloat162float(src[(i - sub) * stride + j]), now);
         reinterpret_cast<uint8_t*>(out + (i - sub) * (D / 8))[j] = (uint8_t)code4<kInt8>(v, v, v, v);
+      }
+  }
+  if (!kInt8 && now == 0.f) {
+    // zeros and infinities, written above, and NaN (the tokens are read again: the registers
+    // are the usual way's)
+#pragma unroll 1
+    for (int i = sub; i < rows; i += kAtOnce)
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) {
+        const float x = __bfloat162float(src[(i - sub) * stride + j]);
+        if (x != x) reinterpret_cast<uint8_t*>(out + (i - sub) * (D / 8))[j] = (uint8_t)code4<false>(x, x, x, x);
       }
   }
   if (tid == 0) *scale = now;

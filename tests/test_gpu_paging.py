@@ -212,6 +212,26 @@ def test_special_values(kind):
     check_write(case, kind)
 
 
+def test_nan_tokens_in_a_block_of_zeros():
+    """e4m3 has a code for them; int8 has none and stores 0."""
+    for kind in KINDS:
+        case = write_case([0, 20], [64, 10], 2, 64, kind, 45)
+        old, new, cu, table, sides = case
+        for x, codes, scale in sides:
+            x[:, 0] = 0
+            x[5, 0, 7] = x[6, 0, 8] = float("nan")
+            x[8, 0, 1], x[9, 0, 2] = float("inf"), float("-inf")
+        (kc, ks), (vc, vs) = write(*case, check_device_status=True)
+        for codes, scale in ((kc, ks), (vc, vs)):
+            page = int(table[0, 0])
+            assert scale[page, 0] == 0
+            got = codes[page, 0].float()
+            nan = torch.zeros(64, 64, dtype=torch.bool)
+            if kind == "e4m3":
+                nan[5, 7] = nan[6, 8] = True
+            assert torch.equal(torch.isnan(got), nan) and (got[~nan] == 0).all()
+
+
 def test_ungranted_requests_are_left_alone():
     old, new, cu, table, sides = write_case([10, 20, 30], [3, 4, 5], 2, 64, "int8", 50)
     import sparse_mla_decoding_b200 as smla
