@@ -369,8 +369,11 @@ typedef struct {
  *                              requests before r) - i].
  * A request fits if its blocks are covered by num_free, its row has room for
  * them, its length stays below 2^31 and its tokens end within max_new_tokens;
- * one that does not keeps its length and its table row, and its tokens get
- * slots -1.
+ * one that does not (a declined request) keeps its length and its table row,
+ * and its tokens get slots -1.  cu_new counts its tokens all the same: their
+ * rows of k, v and q are there, so its seqlens_out - cache_seqlens differs from
+ * cu_new's.  The writer leaves it alone; what smla_gqa_attention_with_kvcache
+ * returns for its rows means nothing.
  *   block_table   : device int32 [batch][max_blocks], fresh entries written
  *   cache_seqlens : device int32 [batch], before the new tokens
  *   new_lens      : device int32 [batch]
@@ -471,7 +474,10 @@ size_t smla_gqa_workspace_bytes(int head_dim, int device);
  *                  written, where the kernel for few tokens would have to read
  *                  2^31 blocks or more
  * h_q is a multiple of h_kv, below 2^20; total_q * h_q < 2^31.  Rows of q that
- * belong to no request are not read and their outputs not written.  A position
+ * belong to no request are not read and their outputs not written.  The n query
+ * tokens are taken to be the last n of cache_seqlens[r]: for a request whose
+ * tokens are not in the cache (one that smla_extend_block_table declined) o and
+ * lse are those of other positions and are to be thrown away.  A position
  * whose block lies outside the table or the cache is skipped and flagged; so is
  * a request whose token offsets run backwards or past total_q (other requests
  * of such a call may be skipped with it).  What the cache holds behind a

@@ -577,9 +577,11 @@ def extend_block_table(block_table: torch.Tensor, cache_seqlens: torch.Tensor, n
     taken from the end; max_new_tokens: length of the slot map.
     Returns (slot_mapping int64 [max_new_tokens], cu_new int32 [b + 1], the lengths with
     the new tokens int32 [b], entries left on the free list int32 [1]).  A request whose
-    blocks or tokens do not fit keeps its length, and its tokens get slots -1, which
-    quantize_kv skips.  slot_mapping goes to quantize_kv; cu_new and the lengths go to
-    quantize_kv_blocks and the attention calls.
+    blocks or tokens do not fit is declined: it keeps its length, and its tokens get slots
+    -1, which quantize_kv skips.  cu_new counts them all the same; quantize_kv_blocks leaves
+    such a request alone, and what gqa_attention_with_kvcache returns for its rows means
+    nothing.  slot_mapping goes to quantize_kv; cu_new and the lengths go to quantize_kv_blocks
+    and the attention calls.
     """
     if not block_table.is_cuda:
         _bad("block_table must be int32 [b, max_blocks] on CUDA")
@@ -729,9 +731,11 @@ def gqa_attention_with_kvcache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 
     q: bf16 [b, s_q, h_q, d], or [total_q, h_q, d] with cu_seqlens_q int32 [b + 1]; a
     request's query tokens are its last positions and are already in the cache, so
-    cache_seqlens (int32 [b]) counts them.  One new token per request, several, or whole
-    prompts: max_seqlen_q (the most query tokens of a request; total_q if not given) only
-    helps to pick the kernel (above total_q: the one for long prompts).
+    cache_seqlens (int32 [b]) counts them (throw the rows of a request away whose tokens
+    extend_block_table declined: they are taken for its last positions too).  One new token
+    per request, several, or whole prompts: max_seqlen_q (the most query tokens of a
+    request; total_q if not given) only helps to pick the kernel (above total_q: the one
+    for long prompts).
     Scores are softmax_scale * <q, k> (default 1/sqrt(d)), then softcap * tanh(x / softcap)
     with softcap > 0, then minus alibi_slopes[h] * distance (float32 [h_q]).
     A token at position p sees j <= p (causal), every j < prefix_lens[r] as well (int32

@@ -345,6 +345,46 @@ def test_serving_steps(kind):
             assert (np.abs(got - x) <= half).all()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("first", [5, 50])
+def test_a_declined_request_leaves_the_step_to_the_others(first, kind):
+    """Tables, writer and attention of a step in which one request gets no blocks: its cache and
+    length stay, nothing is flagged, and the others' results are theirs.  What its own rows of o
+    hold means nothing (their tokens are in no cache)."""
+    import sparse_mla_decoding_b200 as smla
+    h_q, h_kv, d, dev = 8, 2, 64, "cuda"
+    g = torch.Generator(device=dev).manual_seed(11)
+    kc = torch.zeros(9, h_kv, BLOCK, d, dtype=torch.int8, device=dev).view(U.CACHE_TYPES[kind])
+    vc = torch.zeros_like(kc.view(torch.int8)).view(U.CACHE_TYPES[kind])
+    ks, vs = torch.zeros(9, h_kv, device=dev), torch.zeros(9, h_kv, device=dev)
+    table = torch.zeros(3, 8, dtype=torch.int32, device=dev)
+    free = torch.randperm(9, generator=g, device=dev).to(torch.int32)
+    left = torch.tensor([5], dtype=torch.int32, device=dev)
+    lens = torch.zeros(3, dtype=torch.int32, device=dev)
+    for new in ([10, 20, 30], [first, 300, 4]):       # a block each, then room in it, no room, room in it
+        new_lens, n = torch.tensor(new, dtype=torch.int32, device=dev), sum(new)
+        slots, cu, after, left = smla.extend_block_table(table, lens, new_lens, free, left, n)
+        qkv = torch.randn(n, h_q + 2 * h_kv, d, generator=g, device=dev).to(torch.bfloat16)
+        q, k, v = qkv[:, :h_q], qkv[:, h_q:h_q + h_kv], qkv[:, h_q + h_kv:]
+        before = [x.clone() for x in (kc, vc, ks, vs)]
+        smla.quantize_kv_blocks(k, v, kc, vc, ks, vs, table, lens, after, cu, check_device_status=True)
+        lens = after
+        o, lse = smla.gqa_attention_with_kvcache(q, kc, vc, ks, vs, table, lens, cu_seqlens_q=cu,
+                                                 max_seqlen_q=max(new), check_device_status=True)
+    assert lens.tolist() == [10 + first, 20, 34] and int(left) == 2
+    at, page = [0, first, first + 300, first + 304], int(table[1, 0])
+    assert cu.tolist() == at and (slots[at[1]:at[2]] == -1).all() and (slots[:at[1]] >= 0).all()
+    for x, was in zip((kc, vc, ks, vs), before):
+        assert torch.equal(x[page].view(torch.int8), was[page].view(torch.int8))
+    host = [x.cpu() for x in (kc, ks, vc, vs)]
+    K, V = (host[i].double().numpy() * host[i + 1].double().numpy()[:, :, None, None] for i in (0, 2))
+    for r in (0, 2):
+        rows = slice(at[r], at[r + 1])
+        U.compare(o[rows], lse[rows], U.attention(q[rows].double().cpu().numpy(), K, V, table[r:r + 1].cpu().numpy(),
+                                                  lens[r:r + 1].cpu().numpy(), np.array([0, at[r + 1] - at[r]]),
+                                                  v_scale=host[3].double().numpy()))
+
+
 def test_slot_map_drives_the_mla_cache():
     """The same tables and slots for the MLA cache: quantize_kv by slots, then the dense decode."""
     import oracle
