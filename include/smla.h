@@ -374,6 +374,11 @@ typedef struct {
  * rows of k, v and q are there, so its seqlens_out - cache_seqlens differs from
  * cu_new's.  The writer leaves it alone; what smla_gqa_attention_with_kvcache
  * returns for its rows means nothing.
+ * Blocks come back by the caller: where a request ends or is made shorter
+ * (rejected draft tokens), its entries from ceil(length / 64) of the shorter
+ * length on are still its blocks.  Put them behind the first num_free entries
+ * of free_blocks and add them to num_free before the next call, which gives
+ * those entries new blocks without a look at the old ones.
  *   block_table   : device int32 [batch][max_blocks], fresh entries written
  *   cache_seqlens : device int32 [batch], before the new tokens
  *   new_lens      : device int32 [batch]

@@ -580,7 +580,10 @@ def extend_block_table(block_table: torch.Tensor, cache_seqlens: torch.Tensor, n
     blocks or tokens do not fit is declined: it keeps its length, and its tokens get slots
     -1, which quantize_kv skips.  cu_new counts them all the same; quantize_kv_blocks leaves
     such a request alone, and what gqa_attention_with_kvcache returns for its rows means
-    nothing.  slot_mapping goes to quantize_kv; cu_new and the lengths go to quantize_kv_blocks
+    nothing.  Where a request ends or gets shorter (rejected draft tokens), put its table
+    entries from ceil(length / 64) on behind the first num_free of free_blocks and raise
+    num_free before the next call, which overwrites them: nothing else gives blocks back.
+    slot_mapping goes to quantize_kv; cu_new and the lengths go to quantize_kv_blocks
     and the attention calls.
     """
     if not block_table.is_cuda:

@@ -92,6 +92,31 @@ def test_lengths_at_the_end_of_32_bits():
         assert t[0, -3:].tolist() == ref and torch.equal(t[0, :-3], table[0, :-3])
 
 
+def test_shortened_requests_give_their_blocks_back():
+    """Draft tokens are taken back across block edges and a request ends: the caller puts the
+    entries behind the kept length on the free list, and after each step every block is held by
+    one request or free."""
+    import sparse_mla_decoding_b200 as smla
+    rng = np.random.default_rng(12)
+    nb, b, cols = 40, 4, 12
+    table = torch.zeros(b, cols, dtype=torch.int32, device="cuda")
+    free = torch.from_numpy(rng.permutation(nb).astype(np.int32)).cuda()
+    left = torch.tensor([nb], dtype=torch.int32, device="cuda")
+    lens = torch.zeros(b, dtype=torch.int32, device="cuda")
+    col = torch.arange(cols, device="cuda")[None]
+    for step in range(30):
+        new = torch.from_numpy(rng.integers(0, 90, b).astype(np.int32)).cuda()
+        _, _, lens, left = smla.extend_block_table(table, lens, new, free, left, 400)
+        keep = lens - torch.from_numpy(rng.integers(0, 130, b).astype(np.int32)).cuda()
+        keep = torch.where(torch.arange(b, device="cuda") == step % b, 0, keep.clamp(min=0)).to(torch.int32)
+        gone = (col >= (keep[:, None] + 63) // 64) & (col < (lens[:, None] + 63) // 64)
+        back = table[gone]
+        free[int(left):int(left) + len(back)] = back
+        left, lens = left + len(back), keep
+        held = table[col < (lens[:, None] + 63) // 64]
+        assert sorted(held.tolist() + free[:int(left)].tolist()) == list(range(nb))
+
+
 def test_empty_batches():
     tables(np.zeros(0), np.zeros(0), np.arange(3), cols=1)
     tables(np.zeros(0), np.zeros(0), np.arange(3), cols=1, max_new=70)
