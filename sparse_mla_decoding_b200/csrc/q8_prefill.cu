@@ -595,7 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     constexpr int kHalves = D / 64;                   // 64-byte halves of a row of codes
     constexpr int kLoads = 2 * kHalves;               // 16-byte loads of a thread and tile
     const int q = warp - 8, sub = lane >> 2, c4 = lane & 3;
-    // Table entries and scales of 32 blocks, one a lane.
+    // Table entries and scales of 32 blocks, one a lane.  The base, the first value scale above
+    // 0, is looked for in all 32 or block by block (blocks of zeros before it want none): ragged
+    // prompts at d = 128 take 331 us and 340, at d = 64 153 and 148.
     int page = -1;
     float kscale = -1.f, vscale = 0.f, base_log2 = -INFINITY;
     auto load_entries = [&](int b) {                  // block b: this lane's
@@ -612,12 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
           page = -1;
         }
       }
-      if (base_log2 == -INFINITY) {                   // no scale above 0 so far; blocks of zeros want no base
-        const uint32_t above = __ballot_sync(0xffffffffu, vscale > 0.f);
-        const float base = __shfl_sync(0xffffffffu, vscale, above ? __ffs(above) - 1 : 0);
-        base_log2 = log2f(base);
-        if (tid == 256) sm.base = base;
-      }
+      if constexpr (D == 128)
+        if (base_log2 == -INFINITY) {
+          const uint32_t above = __ballot_sync(0xffffffffu, vscale > 0.f);
+          const float base = __shfl_sync(0xffffffffu, vscale, above ? __ffs(above) - 1 : 0);
+          base_log2 = log2f(base);
+          if (tid == 256) sm.base = base;
+        }
     };
     load_entries(lane);
     const int code_off = (head * kBlk + 16 * q + sub) * D + 16 * c4;
@@ -673,6 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
         const int st = i % kStages;
         BlockScales bs;
         bs.k = ks[e];
+        if constexpr (D == 64)
+          if (base_log2 == -INFINITY) {
+            base_log2 = log2f(vs[e]);
+            if (tid == 256) sm.base = vs[e];
+          }
         bs.rel = rel_log2(vs[e], base_log2);
         bs.unrel = ex2(-bs.rel);
         int pg = -1;

@@ -218,6 +218,18 @@ def test_zero_value_scales_before_far_ones(n, size):
         U.compare(o, lse, (o_ref, lse_ref, tol + 2.0 ** -134, tol_lse))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_blocks_of_zeros_before_far_values(d):
+    """More than 32 blocks whose value scale is 0 in one CTA's or warp's run of blocks."""
+    x = build([9] * 10, [2500, 2400] + [60] * 8, 32, 8, d, "int8", 2030 + d, poison=False)
+    zeros = x["table"][:2, :35]
+    x["vs"] *= 2.0 ** -100
+    x["vs"][zeros] = 0
+    x["vc"][zeros] = 0
+    x["v"] = x["vc"].double().numpy() * x["vs"].double().numpy()[:, :, None, None]
+    check(x)
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e30])
 def test_far_query_sizes(size):
     """Queries far outside f16's range: scores of ordinary size come from the softmax scale."""
