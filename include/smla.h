@@ -415,6 +415,9 @@ int smla_extend_block_table(int32_t* block_table, int max_blocks, const int32_t*
  *          infinities too); NaN is stored as NaN (e4m3, for now = 0 too) or 0
  *          (int8), other infinities saturate
  * and where now > was the older codes become round(code * (was / now)).
+ * A power of two lies up to 2x above the smallest scale that fits: int8 codes
+ * then use half of their range, and values are off by up to twice the half step
+ * that the tightest scale would give (e4m3 loses only near its smallest codes).
  * Rows behind the last token are left as they were.  No two requests of a call
  * may write to the same block.
  *   k, v          : device bf16 [total_new][h_kv][head_dim] with the given
@@ -457,8 +460,12 @@ size_t smla_gqa_workspace_bytes(int head_dim, int device);
  *   causal      : j <= p, or j < prefix_lens[r]   (the prefix sees itself in
  *                 both directions)
  *   doc_bounds  : doc_bounds[token][0] <= j < doc_bounds[token][1]
- * q, the probabilities (f16, after an fp32 softmax) and the codes enter the
- * tensor cores, accumulated in fp32.  Output is bitwise reproducible.
+ * q (f16 after a power of two per row: elements below 2^-17 of the row's
+ * largest are off by up to 2^-25 of it), the probabilities (f16 after an fp32
+ * softmax; those below 2^-32 of the largest are dropped) and the codes enter the
+ * tensor cores, accumulated in fp32.  Exponentials are within 3e-6 of their
+ * value, tanh within 4e-7 of softcap; everything else is rounded to fp32.
+ * Output is bitwise reproducible.
  *   q            : device bf16 [total_q][h_q][head_dim] with the given strides
  *                  (elements, multiples of 8), 16-byte aligned
  *   cache        : host struct; read

@@ -30,7 +30,7 @@ constexpr int kQ8SpanTokens = 16;
 // Measured, decode against tensor cores, us, 32 heads over 8, d = 128:
 //   rows of a request      16          32          48          64         128
 //   32 of 4096 tokens   62 / 123   101 / 124   143 / 124   183 / 125
-//   4 of 8192           29 / 38     41 / 38     53 / 39     64 / 39    110 / 47
+//   4 of 8192           26 / 38     37 / 39     48 / 39     58 / 40     98 / 47
 //   1 of 60000          39 / 61     58 / 61     76 / 61     92 / 62    162 / 62
 //   1 of 8192           17 / 20     21 / 20     25 / 20     26 / 21     36 / 21
 //   1 of 8192, 1 head   15 / 18     15 / 18     15 / 18     15 / 18     17 / 18

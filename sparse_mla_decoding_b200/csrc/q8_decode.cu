@@ -22,9 +22,10 @@
 // of 8 heads wastes nothing, where rows on the 16-row side would double the
 // products and the softmax.  The codes go to f16 in registers, once for all rows.
 //
-// Numbers: codes are exact in f16 and q is scaled by a power of two per row, so S
-// has no input rounding and the scales multiply in fp32.  A value scale rides in
-// the exponent,
+// Numbers: codes are exact in f16, and q is scaled by a power of two per row: its
+// elements down to 2^-17 of the row's largest are exact too, smaller ones off by up to
+// 2^-25 of it.  The scales multiply in fp32, exponentials are ex2.approx (2 units in
+// the last place).  A value scale rides in the exponent,
 //   p_j = 2^(x_j + log2 v_scale - m),
 // so one accumulator holds blocks of different scales; the sum of the softmax
 // takes the factor out again per block.  P is rounded to f16 once (2^-11), with m 7 to

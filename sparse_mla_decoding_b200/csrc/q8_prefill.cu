@@ -40,9 +40,9 @@
 // Bound, for 256 rows x 64 keys at d = 128: 1330 clocks of the tensor cores, 1024 of
 // the special function units with all exponentials there (a quarter is on the FMA
 // pipe).  A step takes 1900 (long loops) to 2300 clocks: the chain of a softmax warp
-// from S to P is longer than the products of the other tile.  A CTA takes about 8 us
+// from S to P is longer than the products of the other tile.  A CTA takes 8 to 10 us
 // beside its steps (finding its request, Q, the output), which is what short prompts
-// and documents wait for.  8192 tokens on 8192, 32 heads: 1.46 ms, 1.13 PFLOP/s
+// and documents wait for.  8192 tokens on 8192, 32 heads: 1.5 ms, 1.1 PFLOP/s
 // (1.6 ms where the power cap lowers the clocks).
 #include <cuda_runtime.h>
 
@@ -240,7 +240,8 @@ constexpr int kRowLanes = D / 8;          // lanes that read or write a row of q
 // exponentials that the special function units would be waited for: n = round(x)
 // by adding 1.5 * 2^23, 2^(x - n) by a degree-4 fit in relative error (2.7e-6 at
 // most, 4e-8 in the mean; reweighted least squares on Chebyshev nodes), n added to
-// the exponent field.  Below 2^-126, and for NaN: 2^-126.
+// the exponent field (the idea of Schraudolph, "A fast, compact approximation of the
+// exponential function", 1999).  Below 2^-126, and for NaN: 2^-126.
 __device__ __forceinline__ float2 ex2_poly(float2 x) {
   x.x = fmaxf(x.x, -126.f);
   x.y = fmaxf(x.y, -126.f);

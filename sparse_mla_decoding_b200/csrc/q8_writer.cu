@@ -9,7 +9,10 @@
 // for now = 0 all codes are 0 but those of NaN, which e4m3 keeps at any scale.
 // Powers of two make x / s and the rescaling of e4m3 codes exact (up to the
 // code's own rounding), and a block that fills token by token is rescaled only
-// when its maximum crosses a power of two, not at every new maximum.
+// when its maximum crosses a power of two, not at every new maximum.  The price: a power
+// of two lies up to 2x above the smallest scale that fits.  e4m3 has the exponent for it;
+// of int8's codes up to half stay unused, so a value is off by up to twice the half step of
+// the tightest scale, one bit of eight.
 //
 // One CTA per (block, head, keys or values): the block's new tokens stay in
 // registers between the maximum and the codes, so everything is read and
