@@ -144,6 +144,15 @@ __device__ __forceinline__ void row_pow2(float amax, float& up, float& down) {
   down = __uint_as_float((uint32_t)k << 23);
 }
 
+// m + log2(s) of a softmax sum s > 0 to the reference m, which may both be far from 0 where
+// value scales are (2^60, and zeros count as 2^-60): s's exponent joins m first, so that
+// nothing is rounded at that size.
+__device__ __forceinline__ float lse_log2(float m, float s) {
+  float up, down;
+  row_pow2(s, up, down);
+  return m + (float)((int)(__float_as_uint(down) >> 23) - 127) + log2f(s * up);
+}
+
 // Two fp32 operations in one instruction; each is rounded as the scalar one.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;

@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kWarpsOf<D, NT> * 32, 1)
         const float inv = s == 0.f ? 0.f : 1.f / s;
 #pragma unroll
         for (int k = 0; k < kOut; ++k) O[nt][k][i] *= inv, O[nt][k][2 + i] *= inv;
-        const float lse2 = s == 0.f ? -INFINITY : m[nt][i] + log2f(s);
+        const float lse2 = s == 0.f ? -INFINITY : lse_log2(m[nt][i], s);
         const int in_tile = 8 * nt + 2 * c + i;
         int hh;
         const int t = token_of(e.rt, in_tile, hh), hq = e.head * p.group + hh;

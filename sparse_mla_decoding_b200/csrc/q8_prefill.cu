@@ -567,13 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
           }
         }
         if (part >= 0) {
-          scratch.lse[(int64_t)part * 2 * kTileRows + me] = none ? -INFINITY : m + log2f(l);
+          scratch.lse[(int64_t)part * 2 * kTileRows + me] = none ? -INFINITY : lse_log2(m, l);
         } else {
           int at = -1;                                  // this thread's row of o and lse
           if (row0 + me < rows_all) {
             const int t = (int)(row0 + me) / p.group;
             at = (q0 + t) * p.h_q + head * p.group + (int)(row0 + me) - t * p.group;
-            p.lse[at] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+            p.lse[at] = none ? -INFINITY : lse_log2(m, l) * kLn2;
           }
           __syncwarp();
           const int sub = lane / kRowLanes<D>, chunk = lane % kRowLanes<D>;

@@ -230,6 +230,43 @@ def test_many_blocks_of_zeros_before_far_values(d):
     check(x)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_over_values_of_zero(d):
+    """All value scales 0: o is 0, and lse as precise as ever, of rows that see one key each."""
+    x = build([70], [140], 32, 1, d, "int8", 2050 + d, poison=False)
+    x["vs"].zero_()
+    x["v"] = np.zeros_like(x["v"])
+    at = np.arange(70)
+    o, lse = check(x, softmax_scale=0.003, doc_bounds=np.stack([at, at + 1], 1).astype(np.int32))
+    assert (o == 0).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,d", [(1, 64), (1, 128), (40, 64), (40, 128)])
+def test_values_of_a_zero_scale(n, d, kind):
+    """A block whose codes stand for zeros takes all but e^-20 of the weight: o is what the others
+    give.  A NaN among them is a NaN for the tokens that see it (e4m3)."""
+    x = build([n], [300], 8, 2, d, kind, 2070 + d, poison=False)
+    block = x["table"][0, 0]
+    u = torch.sign(torch.randn(d, generator=torch.Generator().manual_seed(d)))
+    x["q"][:] = u
+    x["kc"][block] = u.to(x["kc"].dtype)
+    x["ks"] *= 0.02
+    x["ks"][block] = 20.0 / d
+    x["vs"][block] = 0
+    x["k"], x["v"] = (x[c].double().numpy() * x[s].double().numpy()[:, :, None, None]
+                      for c, s in (("kc", "ks"), ("vc", "vs")))
+    check(x, softmax_scale=1.0)
+    if kind == "e4m3":
+        x["vc"].view(torch.int8)[block, 0, 5, 3] = 127
+        ref = reference({**x, "v": np.nan_to_num(x["v"])}, softmax_scale=1.0)
+        for hint in (1, LONG):
+            o, lse, _ = call(x, softmax_scale=1.0, max_seqlen_q=hint)
+            assert torch.isnan(o[:, :4, 3]).all() and torch.isfinite(lse).all()
+            o[:, :4, 3] = torch.from_numpy(ref[0]).cuda()[:, :4, 3].to(o.dtype)
+            U.compare(o, lse, ref)
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e30])
 def test_far_query_sizes(size):
     """Queries far outside f16's range: scores of ordinary size come from the softmax scale."""
