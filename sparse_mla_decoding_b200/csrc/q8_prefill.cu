@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const __grid_co
     const int q = warp - 8, sub = lane >> 2, c4 = lane & 3;
     // Table entries and scales of 32 blocks, one a lane.  The base, the first value scale above
     // 0, is looked for in all 32 or block by block (blocks of zeros before it want none): ragged
-    // prompts at d = 128 take 331 us and 340, at d = 64 153 and 148.
+    // prompts at d = 128 took 331 us so and 340, at d = 64 153 and 148.
     int page = -1;
     float kscale = -1.f, vscale = 0.f, base_log2 = -INFINITY;
     auto load_entries = [&](int b) {                  // block b: this lane's
